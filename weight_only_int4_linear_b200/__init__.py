@@ -38,6 +38,12 @@ PATH_AUTO = 0
 PATH_DECODE = 1
 PATH_PREFILL = 2
 
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_SILU = 2
+ACT_GELU = 3
+ACT_GELU_TANH = 4
+
 _lib = None
 
 # C signatures: name -> (restype, argtypes)
@@ -61,6 +67,14 @@ SIGNATURES = {
     "w8a16_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "w8a16_linear": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
     "w4a16_linear_host": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "w4a16_fused_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "w4a16_dx_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "w4a16_linear_fused": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp, _int, _vp, _vp, _vp, _sz,
+                                  _vp]),
+    "w4a16_gated": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _int, _vp, _vp, _vp, _sz, _vp]),
+    "w4a16_linear_dx": (_int, [_vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "w4a16_gated_backward": (_int, [_vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz,
+                                    _vp]),
     "w4a16_unpack": (_int, [_vp, _i64, _i64, _vp, _vp]),
     "w4a16_dequant": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp]),
     "w4a16_dequant_codes": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp]),
@@ -236,6 +250,121 @@ def linear_g(X: torch.Tensor, group: int, qweight: torch.Tensor, scales: torch.T
         _dev(scales, "scales", torch.bfloat16, (N, K // group)), _dev(zeros, "zeros", torch.int32, (N, K // group)),
         N, _dev(Y, "Y", torch.bfloat16, (M, N)), ws_ptr, ws_bytes, _stream(stream))
     _check("w4a16_linear_g", st)
+
+
+def fused_workspace_bytes(M: int, N: int, K: int, group: int = GROUP) -> int:
+    """w4a16_fused_workspace_bytes: for linear_fused and gated (N: weight rows)."""
+    return int(load().w4a16_fused_workspace_bytes(M, N, K, group))
+
+
+def dx_workspace_bytes(M: int, N: int, K: int, group: int = GROUP) -> int:
+    """w4a16_dx_workspace_bytes: for linear_dx and gated_backward (N: weight rows)."""
+    return int(load().w4a16_dx_workspace_bytes(M, N, K, group))
+
+
+class _On:
+    """Marshals tensors that must share one CUDA device; `call` runs with that device current, on `stream` (None:
+    the device's current stream)."""
+
+    __slots__ = ("device",)
+
+    def __init__(self, t: torch.Tensor, name: str):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        self.device = t.device
+
+    def ptr(self, t, name: str, dtype, shape=None) -> int:
+        p = _dev(t, name, dtype, shape)
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, is on {t.device}")
+        return p
+
+    def opt(self, t, name: str, dtype, shape):
+        return None if t is None else self.ptr(t, name, dtype, shape)
+
+    def weight(self, qweight, scales, zeros, N: int, K: int, group: int):
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        return (self.ptr(qweight, "qweight", torch.int32, (N, K // 8)),
+                self.ptr(scales, "scales", torch.bfloat16, (N, K // group)),
+                self.ptr(zeros, "zeros", torch.int32, (N, K // group)))
+
+    def call(self, name: str, stream, *args) -> None:
+        if isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
+            raise ValueError(f"stream must be on {self.device}, is on {stream.device}")
+        fn = getattr(load(), name)
+        if self.device.index == torch.cuda.current_device():
+            st = fn(*args, _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, _stream(stream))
+        _check(name, st)
+
+
+def _two_dims(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.shape
+
+
+def linear_fused(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, Y: torch.Tensor,
+                 workspace: torch.Tensor, bias: torch.Tensor | None = None, act: int = ACT_NONE,
+                 residual: torch.Tensor | None = None, group: int = GROUP, inv_s: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """w4a16_linear_fused: Y[M, N] = act(X[M, K] . W_hat^T + bias) + residual (residual may be Y itself); with inv_s,
+    X is first replaced by bf16(X * inv_s).  workspace: zeroed once, >= fused_workspace_bytes(M, N, K, group)."""
+    on = _On(X, "X")
+    M, K = _two_dims(X, "X")
+    N = qweight.shape[0]
+    on.call("w4a16_linear_fused", stream, on.ptr(X, "X", torch.bfloat16), on.opt(inv_s, "inv_s", torch.float32, (K,)),
+            M, K, group, *on.weight(qweight, scales, zeros, N, K, group), N,
+            on.opt(bias, "bias", torch.bfloat16, (N,)), act, on.opt(residual, "residual", torch.bfloat16, (M, N)),
+            on.ptr(Y, "Y", torch.bfloat16, (M, N)), on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
+
+
+def gated(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, H: torch.Tensor,
+          workspace: torch.Tensor, act: int = ACT_SILU, GU: torch.Tensor | None = None, group: int = GROUP,
+          inv_s: torch.Tensor | None = None, stream=None) -> None:
+    """w4a16_gated: H[M, I] = act(G) * U with [G | U] = X . W_hat^T, the packed weight holding I gate rows and then I
+    up rows; GU [M, 2 I] receives [G | U] when given (gated_backward needs it)."""
+    on = _On(X, "X")
+    M, K = _two_dims(X, "X")
+    N = qweight.shape[0]
+    if N % 2:
+        raise ValueError("a gated weight has an even number of rows")
+    on.call("w4a16_gated", stream, on.ptr(X, "X", torch.bfloat16), on.opt(inv_s, "inv_s", torch.float32, (K,)), M, K,
+            group, *on.weight(qweight, scales, zeros, N, K, group), N, act,
+            on.ptr(H, "H", torch.bfloat16, (M, N // 2)), on.opt(GU, "GU", torch.bfloat16, (M, N)),
+            on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
+
+
+def linear_dx(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, dX: torch.Tensor,
+              workspace: torch.Tensor, group: int = GROUP, inv_s: torch.Tensor | None = None, stream=None) -> None:
+    """w4a16_linear_dx: dX[M, K] = dY[M, N] . W_hat (times inv_s per column when given), the gradient of the layer's
+    input.  workspace: >= dx_workspace_bytes(M, N, K, group)."""
+    on = _On(dY, "dY")
+    M, N = _two_dims(dY, "dY")
+    K = qweight.shape[1] * 8
+    on.call("w4a16_linear_dx", stream, on.ptr(dY, "dY", torch.bfloat16), M, N, group,
+            *on.weight(qweight, scales, zeros, N, K, group), K, on.opt(inv_s, "inv_s", torch.float32, (K,)),
+            on.ptr(dX, "dX", torch.bfloat16, (M, K)), on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
+
+
+def gated_backward(dH: torch.Tensor, GU: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                   zeros: torch.Tensor, dGU: torch.Tensor, dX: torch.Tensor, workspace: torch.Tensor,
+                   act: int = ACT_SILU, group: int = GROUP, inv_s: torch.Tensor | None = None, stream=None) -> None:
+    """w4a16_gated_backward: dGU = [dH * U * act'(G) | dH * act(G)] (may be GU itself) and dX[M, K] = dGU . W_hat,
+    the gradient of gated's input.  workspace: >= dx_workspace_bytes(M, N, K, group)."""
+    on = _On(dH, "dH")
+    M, I = _two_dims(dH, "dH")
+    N, K = qweight.shape[0], qweight.shape[1] * 8
+    if N != 2 * I:
+        raise ValueError("the weight must have two rows for every column of dH")
+    on.call("w4a16_gated_backward", stream, on.ptr(dH, "dH", torch.bfloat16),
+            on.ptr(GU, "GU", torch.bfloat16, (M, N)), M, N, act, group,
+            *on.weight(qweight, scales, zeros, N, K, group), K, on.opt(inv_s, "inv_s", torch.float32, (K,)),
+            on.ptr(dGU, "dGU", torch.bfloat16, (M, N)), on.ptr(dX, "dX", torch.bfloat16, (M, K)),
+            on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
 
 
 def w8_quantize(W: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, dev_status: torch.Tensor,

@@ -161,14 +161,16 @@ struct DecodePlan {
     size_t workspace_bytes() const;
 };
 DecodePlan plan_decode(int64_t M, int64_t N, int64_t K, int num_sms);
+struct FusedEpilogue;  // epilogue.cuh
 // xscale (nullable, [K] FP32): the AWQ activation transform, x -> bf16(x * xscale[k]), applied
 // where each path prepares X.
 // X_host, Y_host (nullable, one-token plans only): device addresses of mapped page-locked host buffers; X is
 // then first copied from X_host into X by a kernel of the launch chain, and Y is also stored into Y_host.
+// ep (nullable, plans with cc_tokens or mt): Y is what the fused epilogue makes of the sums.
 int launch_decode(const uint16_t* X, const float* xscale, int64_t M, int64_t K, const uint32_t* qweight,
                   const uint16_t* scales, const int32_t* zeros, int64_t N, uint16_t* Y, void* workspace,
                   const DecodePlan& plan, cudaStream_t stream, const uint16_t* X_host = nullptr,
-                  uint16_t* Y_host = nullptr);
+                  uint16_t* Y_host = nullptr, const FusedEpilogue* ep = nullptr);
 int num_sms_current();
 
 // The BF16 tensor-core GEMV (gemv_bf.cu) for quantisation groups of `group` (32, 64, 128) weights, K / group
@@ -194,7 +196,7 @@ bool mt_supported(int64_t K);
 size_t mt_workspace_bytes(int64_t M, int64_t N, int64_t K, int num_sms);
 int launch_decode_mt(const uint16_t* X, const float* xscale, int64_t M, int64_t K, const uint32_t* qweight,
                      const uint16_t* scales, const int32_t* zeros, int64_t N, uint16_t* Y, void* scratch,
-                     cudaStream_t stream);
+                     cudaStream_t stream, const FusedEpilogue* ep = nullptr);
 
 // Prefill (tensor-core GEMM) path for large M.
 constexpr int64_t kPrefillMinM = 64;  // W4A16_PATH_AUTO switches to the GEMM at this many tokens
@@ -211,7 +213,7 @@ int launch_quantize_pack_small(const float* W, int64_t N, int64_t K, int group, 
 size_t decode_sub_workspace_bytes(int64_t N, int64_t K, int group);
 int launch_decode_sub(const uint16_t* X, int64_t M, int64_t K, int group, const uint32_t* qweight,
                       const uint16_t* scales, const int32_t* zeros, int64_t N, uint16_t* Y, void* workspace,
-                      cudaStream_t stream);
+                      cudaStream_t stream, const FusedEpilogue* ep = nullptr);
 
 // W8A16: INT8 weights with one BF16 scale per row (w8.cu).
 size_t w8_workspace_bytes(int64_t M, int64_t N, int64_t K);

@@ -1,0 +1,104 @@
+// Epilogues of the fused linear layer, the gated feed-forward projection and
+// their backward pass: activation functions, and what each output element
+// goes through after its FP32 sum.
+#pragma once
+#include "common.cuh"
+
+#include "../../include/w4a16_fused.h"
+
+namespace w4a16 {
+
+// What follows the product X . W_hat^T.  gated == 0: Y = act(sum + bias) + residual, each optional.
+// gated == 1: the weight holds I gate rows and then I up rows, Y[m][j] = act(sum_j) * sum_{I + j}, and GU
+// (nullable) keeps both sums.  Everything in FP32, one rounding to BF16 at each store.
+struct FusedEpilogue {
+    const uint16_t* bias;      // [N] or null
+    const uint16_t* residual;  // [M][N] or null; may be Y itself
+    uint16_t* GU;              // [M][2 I] or null
+    int act;
+    int gated;
+};
+
+// 1 / (1 + e^-x).  __expf's error grows as 2^-22 |x|, far below the 2^-9 of the BF16 store; e^-x overflowing to
+// infinity gives the limit 0.
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+constexpr float kRsqrt2 = 0.7071067811865476f;
+constexpr float kRsqrt2Pi = 0.3989422804014327f;
+
+// act(x).  GELU by erfc and by a sigmoid (0.5 (1 + tanh u) = sigmoid(2 u)): neither form cancels for negative x.
+__device__ __forceinline__ float act_f(float x, int act) {
+    switch (act) {
+        case W4A16_ACT_RELU: return x < 0.f ? 0.f : x;  // NaN stays NaN
+        case W4A16_ACT_SILU: return x < -88.f ? x * __expf(x) : x * sigmoid_f(x);
+        case W4A16_ACT_GELU: return 0.5f * x * erfcf(-x * kRsqrt2);
+        case W4A16_ACT_GELU_TANH: {
+            const float u = 2.f * kGeluC * (x + kGeluA * x * x * x);
+            return u < -88.f ? x * __expf(u) : x * sigmoid_f(u);
+        }
+        default: return x;
+    }
+}
+
+// act(x) and act'(x).
+__device__ __forceinline__ void act_grad_f(float x, int act, float& f, float& d) {
+    switch (act) {
+        case W4A16_ACT_RELU:
+            f = x < 0.f ? 0.f : x;
+            d = x > 0.f ? 1.f : 0.f;  // 0 at 0
+            return;
+        case W4A16_ACT_SILU: {
+            const float s = x < -88.f ? __expf(x) : sigmoid_f(x), t = sigmoid_f(-x);
+            f = x * s;
+            d = s * (1.f + x * t);
+            return;
+        }
+        case W4A16_ACT_GELU: {
+            const float p = 0.5f * erfcf(-x * kRsqrt2);
+            f = x * p;
+            d = p + x * kRsqrt2Pi * __expf(-0.5f * x * x);
+            return;
+        }
+        case W4A16_ACT_GELU_TANH: {
+            const float x2 = x * x, u = 2.f * kGeluC * (x + kGeluA * x2 * x);
+            const float s = u < -88.f ? __expf(u) : sigmoid_f(u), t = sigmoid_f(-u);
+            f = x * s;
+            // s t vanishes long before the cubic factor overflows; past |x| = 30 it is zero in FP32
+            d = fabsf(x) > 30.f ? s : s + x * s * t * 2.f * kGeluC * (1.f + 3.f * kGeluA * x2);
+            return;
+        }
+        default:
+            f = x;
+            d = 1.f;
+    }
+}
+
+// One output of the plain epilogue: n the weight row, off = m N + n.
+__device__ __forceinline__ float linear_epilogue(float v, const FusedEpilogue& e, float bias, float residual) {
+    return act_f(v + bias, e.act) + residual;
+}
+
+// BF16 load from L2, never the non-coherent path: the residual may be Y, which this kernel writes.
+__device__ __forceinline__ float load_bf16(const uint16_t* p) { return bf16_bits_to_float(__ldcg(p)); }
+
+// Host side (epilogue.cu): the split-K slots of the decode GEMVs added and finished.
+// One token: slots [tile][slot][128] in two regions, as decode_cc_reduce_kernel reads them.
+int launch_cc_epilogue(const float* partial, const FusedEpilogue& e, uint16_t* Y, int64_t N, int cpt, int row_tiles,
+                       int tiles_a, int cpt_b, cudaStream_t stream);
+// 2-16 tokens: slots [tile][max_slots][M][128], every row tile's sums in slots.
+int launch_deal_epilogue(const float* partial, const FusedEpilogue& e, uint16_t* Y, int64_t N, int M, int G,
+                         int units_base, int units_rem, int max_slots, int row_tiles, cudaStream_t stream);
+
+// The FP16-operand GEMM (gemm_h.cu), any M, K a multiple of 128, groups of 32, 64 or 128.
+size_t gemm_h_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, bool backward, int num_sms);
+int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, int group, const uint32_t* qweight,
+                  const uint16_t* scales, const int32_t* zeros, int64_t N, const FusedEpilogue& e, uint16_t* Y,
+                  void* workspace, cudaStream_t stream);
+// dX = dY . W_hat (times inv_s per column).  With dH (then dY == null): dY = [dG | dU] formed from dH and GU and
+// also written to dGU.
+int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU, int act, uint16_t* dGU, int64_t M,
+                     int64_t N, int group, const uint32_t* qweight, const uint16_t* scales, const int32_t* zeros,
+                     int64_t K, const float* inv_s, uint16_t* dX, void* workspace, cudaStream_t stream);
+}  // namespace w4a16

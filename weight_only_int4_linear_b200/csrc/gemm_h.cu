@@ -1,0 +1,1029 @@
+// The tensor-core GEMM of the fused operators, in both directions of the layer:
+//   forward   Y[m][n]  = epilogue( sum_k X[m][k] W[n][k] )     (contraction along K)
+//   backward  dX[m][k] = sum_n dY[m][n] W[n][k]                (contraction along N)
+// from the same packed codes, W = (q - z) s dequantised tile by tile on chip.
+//
+// Arithmetic.  Both operands are FP16, prepared so that nothing that matters
+// leaves FP16's range:
+//   * weights: row n is scaled by 2^-e_n, e_n chosen from the row's own scales
+//     and zero points so that |W'| < 2^15.  q - z is formed exactly (1024 + q as
+//     a bit pattern, one packed subtraction) and multiplied once by
+//     s' = s 2^-e_n (8 significant bits, exact in FP16): one rounding of at most 2^-11
+//     of the value.  Backward, 2^e_n cannot leave the sum, so it goes into dY's
+//     column n.
+//   * tokens: row m is scaled by 2^-a_m so that its largest value is in
+//     [2^14, 2^15); BF16 values (8 significant bits) are then exact down to 2^-29
+//     of the row's maximum and lose absolute bits of 2^-40 of it below.
+// Sums run in FP32 in tensor memory over the whole contraction, without a fold
+// per group, and the exponents come back in the epilogue.  Against rounding
+// (q - z) s to BF16 (2^-9) this keeps the outputs' error at that of their own
+// rounding.
+//
+// Tile: 256 output rows (weight rows, or K columns backward) x NT tokens by a
+// cluster of two CTAs with the pair MMA (M = 256); each CTA dequantises its 128
+// rows and holds half of the tile's tokens.  Stages of 64 along the contraction.
+// Forward, a thread's 4 code words are 32 consecutive k of one row: the K-major
+// operand (K order (0,4,1,5,2,6,3,7) in every 8-block, which the token operand
+// is prepared in).  Backward, the same words are 32 consecutive output rows of
+// one contraction step: the MN-major operand, its rows in that order, which the
+// epilogue undoes in its addresses.
+//
+// Work: full waves of tiles run whole, so that the clusters sweep the same
+// operands together (L2); the last, partial wave's tiles are cut along the
+// contraction into equal ranges over all clusters, whose FP32 partial tiles a
+// dependent kernel adds in a fixed order.  With few tokens every tile is cut.
+//
+// Gated weights (I gate rows, then I up rows) are read interleaved by a 3-D
+// tensor map, row 2 j + p = row p I + j, so that a pair of neighbouring lanes
+// holds both sums of an output.
+//
+// Warps (448 threads): 0-7 dequantise, 8-11 epilogue (TMEM lane quadrants), 12
+// TMA, 13 MMA issue (rank 0).  Two accumulators: a tile's epilogue overlaps the
+// next tile's MMAs.
+#include "decode_units.cuh"
+#include "epilogue.cuh"
+#include "sm100.cuh"
+
+#include <cuda_fp16.h>
+
+namespace w4a16 {
+namespace {
+
+constexpr int kBM = 128;                       // output rows per CTA
+constexpr int kTileRows = 2 * kBM;             // per cluster
+constexpr int kBK = 64;                        // contraction per stage
+constexpr int kABytes = kBM * kBK * 2;         // 16 KB
+constexpr int kCodeBytes = kBM * kBK / 2;      // 4 KB
+constexpr int kMetaBytes = 1024;               // up to 8 lines of 128 B x ... (see meta words below)
+constexpr int kDqWarps = 8, kEpiWarps = 4;
+constexpr int kTmaWarp = kDqWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32;  // 448
+constexpr int kTopExp = 15;                    // scaled operands stay below 2^15
+
+enum Mode { kLinear = 0, kGated = 1, kDx = 2 };
+
+template <int NT>
+struct Cfg {
+    static constexpr int kXBytes = NT / 2 * kBK * 2;
+    static constexpr int kStageBytes = kXBytes + kABytes + kCodeBytes + kMetaBytes;
+    static constexpr int kFit = 226 * 1024 / kStageBytes;
+    static constexpr int kStages = kFit < 9 ? kFit : 9;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;  // + alignment slack
+    static constexpr uint32_t kTmemCols = 2 * NT;                          // two accumulators
+    static_assert(kStageBytes % 1024 == 0 && kSmem + 512 <= 232448, "shared memory per CTA");
+};
+
+// Instruction descriptor, kind::f16 with FP16 A and B and an FP32 accumulator; A MN-major for the backward.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn) {
+    return (1u << 4) | (a_mn ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// MN-major operand, 128-byte swizzle: atoms of 64 rows x 8 contraction steps (1024 B, one 128-byte line per
+// step, 16-byte chunk c of step k at c ^ (k % 8)); the next 8 steps 1024 B on, the next 64 rows 8 KB on.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFF);
+    d |= (uint64_t)(8192 >> 4) << 16;  // leading byte offset: next 64 rows
+    d |= (uint64_t)(1024 >> 4) << 32;  // stride byte offset: next 8 steps
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// x 2^t for any t: two exact factors, so that only the result can leave the FP32 range.
+__device__ __forceinline__ float scale2(float x, int t) {
+    t = min(max(t, -280), 252);
+    const int h = t >> 1;
+    return x * pow2f(h) * pow2f(t - h);
+}
+
+// Output row v of a gated weight's interleaved order -> weight row.
+__device__ __forceinline__ int64_t gated_row(int64_t v, int64_t I) { return (v & 1) * I + (v >> 1); }
+
+// ------------------------------------------------------------------ preparation
+//
+// Meta words, [K / group][Rp] (Rp: rows padded to 256): low half s' = s 2^-e (FP16), high half 1024 + z (FP16,
+// exact for |z| <= 1024).  A zero point beyond that leaves 0x7FFF (a NaN) in the high half and e in the low
+// half: the dequantiser then forms the value in binary64 from the stored scale and zero point.  Rows past the
+// matrix get zero words (s' = 0).  exps[v] = e of row v.
+constexpr int kPrepThreads = 256;
+constexpr int kMetaRows = 32;  // rows per block
+
+struct MetaArgs {
+    const uint16_t* scales;
+    const int32_t* zeros;
+    uint32_t* meta;
+    int* exps;
+    int R, Rp, GQ;
+    int64_t I;  // gated: rows per half, else 0
+};
+
+__device__ __forceinline__ int bf16_exponent(uint32_t bits) {  // floor(log2 |x|), or below it for subnormals
+    const int ef = (int)((bits >> 7) & 0xFF);
+    return ef == 0 ? -126 : ef - 127;
+}
+
+__device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
+    __shared__ uint32_t s_word[kMetaRows][33];
+    __shared__ int s_exp[kMetaRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int v0 = block * kMetaRows;
+    constexpr int RPW = kMetaRows / (kPrepThreads / 32);  // rows per warp
+    for (int i = 0; i < RPW; ++i) {
+        const int v = v0 + warp * RPW + i;
+        int top = -100000;
+        if (v < a.R) {
+            const int64_t n = a.I ? gated_row(v, a.I) : v;
+            for (int g = lane; g < a.GQ; g += 32) {
+                const uint32_t sb = __ldg(a.scales + n * a.GQ + g);
+                const long long z = __ldg(a.zeros + n * a.GQ + g);
+                const long long mag = max(z < 0 ? -z : z, 15 - z < 0 ? z - 15 : 15 - z);
+                // |(q - z) s| < 2^(exponent + 1 + bits of mag)
+                if (sb & 0x7FFFu) top = max(top, bf16_exponent(sb) + 1 + (64 - __clzll(mag)));
+            }
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (lane == 0) {
+            const int e = top == -100000 ? 0 : top - kTopExp;
+            s_exp[warp * RPW + i] = e;
+            if (v < a.Rp) a.exps[v] = e;
+        }
+    }
+    __syncthreads();
+    for (int g0 = 0; g0 < a.GQ; g0 += 32) {
+        for (int i = 0; i < RPW; ++i) {
+            const int r = warp * RPW + i, v = v0 + r, g = g0 + lane;
+            uint32_t word = 0;
+            if (v < a.R && g < a.GQ) {
+                const int64_t n = a.I ? gated_row(v, a.I) : v;
+                const int z = __ldg(a.zeros + n * a.GQ + g), e = s_exp[r];
+                if (z >= -1024 && z <= 1024) {
+                    const float s = scale2(bf16_bits_to_float(__ldg(a.scales + n * a.GQ + g)), -e);
+                    word = (uint32_t)__half_as_ushort(__float2half_rn(s)) |
+                           ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16);
+                } else {
+                    word = ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
+                }
+            }
+            s_word[r][lane] = word;
+        }
+        __syncthreads();
+        for (int g = warp; g < 32 && g0 + g < a.GQ; g += kPrepThreads / 32)
+            if (v0 + lane < a.Rp) a.meta[(int64_t)(g0 + g) * a.Rp + v0 + lane] = s_word[lane][g];
+        __syncthreads();
+    }
+}
+
+// The largest exponent over the block, of per-thread values.
+__device__ __forceinline__ int block_max(int v) {
+    __shared__ int s_max[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    __syncthreads();
+    if (lane == 0) s_max[warp] = v;
+    __syncthreads();
+    v = lane < (int)(blockDim.x >> 5) ? s_max[lane] : -100000;
+    return __reduce_max_sync(0xFFFFFFFFu, v);
+}
+
+// Row exponent a from the largest exponent E (|x| < 2^(E + 1)): x 2^-a < 2^15.
+__device__ __forceinline__ int row_exp(int E) { return E == -100000 ? 0 : E + 1 - kTopExp; }
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct TokenArgs {
+    const uint16_t* X;
+    const float* xscale;
+    __half* Xh;  // [M][K], 8-blocks in MMA order, scaled by 2^-a
+    int* texp;   // [M] a
+    int M, K;
+};
+
+// Forward preparation: the first meta_blocks blocks write the weights' meta words, the others one token each.
+__global__ void __launch_bounds__(kPrepThreads) prep_forward_kernel(const MetaArgs ma, int meta_blocks,
+                                                                    const TokenArgs t) {
+    pdl_launch_dependents();
+    pdl_wait_primary();  // X of an earlier kernel; the workspace's earlier readers
+    if ((int)blockIdx.x < meta_blocks) {
+        meta_block(ma, blockIdx.x);
+        return;
+    }
+    const int m = blockIdx.x - meta_blocks;
+    const uint4* x = reinterpret_cast<const uint4*>(t.X + (int64_t)m * t.K);
+    uint4* out = reinterpret_cast<uint4*>(t.Xh + (int64_t)m * t.K);
+    const int n8 = t.K / 8;
+    auto load = [&](int i) {
+        uint4 v = x[i];
+        if (t.xscale) {
+            const float4* r = reinterpret_cast<const float4*>(t.xscale) + 2 * i;
+            const float4 r0 = __ldg(r), r1 = __ldg(r + 1);
+            v = make_uint4(bf16x2_scaled(v.x, r0.x, r0.y), bf16x2_scaled(v.y, r0.z, r0.w),
+                           bf16x2_scaled(v.z, r1.x, r1.y), bf16x2_scaled(v.w, r1.z, r1.w));
+        }
+        return v;
+    };
+    uint32_t top = 0;  // largest magnitude as BF16 bits
+    for (int i = threadIdx.x; i < n8; i += kPrepThreads) {
+        const uint4 v = load(i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    }
+    const int a = row_exp(block_max(top ? bf16_exponent(top) : -100000));
+    const int h = -a >> 1;
+    const float f1 = pow2f(h), f2 = pow2f(-a - h);  // |a| <= 150: both factors are FP32 powers of two
+    if (threadIdx.x == 0) t.texp[m] = a;
+    for (int i = threadIdx.x; i < n8; i += kPrepThreads) {
+        const uint4 v = load(i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(w[j] << 16) * f1 * f2;
+            f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * f1 * f2;
+        }
+        out[i] = make_uint4(half2_bits(f[0], f[4]), half2_bits(f[1], f[5]), half2_bits(f[2], f[6]),
+                            half2_bits(f[3], f[7]));
+    }
+}
+
+__global__ void __launch_bounds__(kPrepThreads) prep_meta_kernel(const MetaArgs ma) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    meta_block(ma, blockIdx.x);
+}
+
+// Backward preparation, one block per token: the FP16 operand D'[m][n] = dY[m][n] 2^(e_n - a_m), row stride Np.
+// dY is read, or (dH given) formed as [dG | dU] from dH and GU = [G | U] and also stored as BF16:
+//   dG = dH U act'(G),  dU = dH act(G).
+// Two passes over the row (the second from L2): the row's exponent first, then the values; dGU may be GU itself,
+// since a thread reads its elements of GU in the second pass before it writes them.  V: elements per load, 8 or 1.
+struct GradArgs {
+    const uint16_t* dY;
+    const uint16_t* dH;
+    const uint16_t* GU;
+    uint16_t* dGU;
+    const int* exps;  // [>= N] e_n
+    __half* Dh;
+    int* texp;
+    int N, I, act;
+    int64_t Np;
+};
+constexpr int kGradThreads = 512;
+
+template <int V>
+__device__ __forceinline__ void load_bf(const uint16_t* p, float (&f)[V]) {
+    if constexpr (V == 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(w[j] << 16);
+            f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    } else {
+        f[0] = bf16_bits_to_float(*p);
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_bf(uint16_t* p, const float (&f)[V]) {
+    if constexpr (V == 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = (uint32_t)float_to_bf16_bits(f[2 * j]) | ((uint32_t)float_to_bf16_bits(f[2 * j + 1]) << 16);
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        *p = float_to_bf16_bits(f[0]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_exps(const int* p, int (&e)[V]) {
+    if constexpr (V == 8) {
+        const int4 a = __ldcg(reinterpret_cast<const int4*>(p)), b = __ldcg(reinterpret_cast<const int4*>(p + 4));
+        e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w;
+        e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
+    } else {
+        e[0] = __ldcg(p);
+    }
+}
+// exponent of an FP32 value plus e; zero counts as nothing
+__device__ __forceinline__ int exp_of(float x, int e) {
+    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+    return u == 0 ? -100000 : max((int)(u >> 23), 1) - 127 + e;
+}
+template <int V>
+__device__ __forceinline__ void store_half(__half* p, const float (&f)[V], const int (&e)[V], int a) {
+    if constexpr (V == 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = half2_bits(scale2(f[2 * j], e[2 * j] - a), scale2(f[2 * j + 1], e[2 * j + 1] - a));
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        *p = __float2half_rn(scale2(f[0], e[0] - a));
+    }
+}
+
+template <int V, bool GATED>
+__global__ void __launch_bounds__(kGradThreads) prep_grad_kernel(const GradArgs g) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const int64_t m = blockIdx.x;
+    __half* out = g.Dh + m * g.Np;
+    int top = -100000;
+    if constexpr (GATED) {
+        const uint16_t *dh = g.dH + m * g.I, *gu = g.GU + m * g.N;
+        uint16_t* dgu = g.dGU + m * g.N;
+        auto grads = [&](int i, float (&dg)[V], float (&du)[V]) {
+            float d[V], gg[V], uu[V];
+            load_bf<V>(dh + i, d);
+            load_bf<V>(gu + i, gg);
+            load_bf<V>(gu + g.I + i, uu);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float f, df;
+                act_grad_f(gg[j], g.act, f, df);
+                dg[j] = d[j] * uu[j] * df;
+                du[j] = d[j] * f;
+            }
+        };
+        for (int i = threadIdx.x * V; i < g.I; i += kGradThreads * V) {
+            float dg[V], du[V];
+            int eg[V], eu[V];
+            grads(i, dg, du);
+            load_exps<V>(g.exps + i, eg);
+            load_exps<V>(g.exps + g.I + i, eu);
+#pragma unroll
+            for (int j = 0; j < V; ++j) top = max(top, max(exp_of(dg[j], eg[j]), exp_of(du[j], eu[j])));
+        }
+        const int a = row_exp(block_max(top));
+        if (threadIdx.x == 0) g.texp[m] = a;
+        for (int i = threadIdx.x * V; i < g.I; i += kGradThreads * V) {
+            float dg[V], du[V];
+            int eg[V], eu[V];
+            grads(i, dg, du);
+            load_exps<V>(g.exps + i, eg);
+            load_exps<V>(g.exps + g.I + i, eu);
+            store_bf<V>(dgu + i, dg);
+            store_bf<V>(dgu + g.I + i, du);
+            store_half<V>(out + i, dg, eg, a);
+            store_half<V>(out + g.I + i, du, eu, a);
+        }
+    } else {
+        const uint16_t* dy = g.dY + m * g.N;
+        for (int i = threadIdx.x * V; i < g.N; i += kGradThreads * V) {
+            float d[V];
+            int e[V];
+            load_bf<V>(dy + i, d);
+            load_exps<V>(g.exps + i, e);
+#pragma unroll
+            for (int j = 0; j < V; ++j) top = max(top, exp_of(d[j], e[j]));
+        }
+        const int a = row_exp(block_max(top));
+        if (threadIdx.x == 0) g.texp[m] = a;
+        for (int i = threadIdx.x * V; i < g.N; i += kGradThreads * V) {
+            float d[V];
+            int e[V];
+            load_bf<V>(dy + i, d);
+            load_exps<V>(g.exps + i, e);
+            store_half<V>(out + i, d, e, a);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the GEMM
+
+struct HArgs {
+    const uint32_t* meta;
+    const int* exps;      // forward: e of every output row
+    const int* texp;      // a of every token
+    const uint16_t* scales;
+    const int32_t* zeros;
+    const float* inv_s;   // backward: per output column, or null
+    uint16_t* Y;          // Y, H or dX
+    float* partial;       // [2 units][NT][256]
+    int* fault;
+    FusedEpilogue ep;
+    int64_t I;            // gated: rows per half
+    int M, R, C;          // tokens, output rows, contraction
+    int Rp, GQ, group, N; // meta stride, groups per weight row, group size, weight rows
+    int NS;               // stages per tile
+    int m_tiles, r_tiles;
+    int whole_tiles;      // tiles 0 .. whole_tiles - 1 run whole: cluster b takes b, b + units, ...
+    int units;            // clusters
+    int base, rem, split_units;  // the other tiles' stages, dealt in equal ranges to the first split_units clusters
+};
+
+constexpr int kRaster = 4;
+__device__ __forceinline__ void tile_coords(int t, const HArgs& a, int& rt, int& mt) {
+    const int per_group = kRaster * a.r_tiles;
+    const int grp = t / per_group, r = t - grp * per_group;
+    const int gm = min(kRaster, a.m_tiles - grp * kRaster);
+    rt = r / gm;
+    mt = grp * kRaster + (r - rt * gm);
+}
+
+// Cluster b's segments: its whole tiles, then its range of the cut tiles' stages.
+struct Segments {
+    int tile, s0, s1;  // the current segment: stages s0 .. s1 - 1 of tile
+    int next_whole;
+    int64_t u, u_end;
+    __device__ __forceinline__ Segments(int b, const HArgs& a) : tile(0), s0(0), s1(0), next_whole(b) {
+        u = u_end = 0;
+        if (b < a.split_units) {
+            u = (int64_t)b * a.base + min(b, a.rem);
+            u_end = u + a.base + (b < a.rem ? 1 : 0);
+        }
+    }
+    __device__ __forceinline__ bool next(const HArgs& a) {
+        if (next_whole < a.whole_tiles) {
+            tile = next_whole;
+            s0 = 0;
+            s1 = a.NS;
+            next_whole += a.units;
+            return true;
+        }
+        if (u >= u_end) return false;
+        const int r = (int)(u / a.NS);
+        tile = a.whole_tiles + r;
+        s0 = (int)(u - (int64_t)r * a.NS);
+        s1 = (int)min((int64_t)a.NS, (int64_t)s0 + (u_end - u));
+        u += s1 - s0;
+        return true;
+    }
+};
+// Slot of cluster b's part of a cut tile that starts at stage s0: a cluster's range has at most one part that
+// starts inside a tile (its first) and one that starts a tile and does not end it (its last).
+__device__ __forceinline__ int slot_of(int b, int s0) { return 2 * b + (s0 == 0 ? 1 : 0); }
+
+// Finishes T tokens of one output row: sum[j] belongs to token m0 + j and output row v.  All lanes of a warp call
+// it together, with consecutive v from an even one (gated rows are exchanged between neighbours).
+template <int MODE, int T>
+__device__ __forceinline__ void finish(const HArgs& a, float (&sum)[T], int m0, int v, float bias, int row_e,
+                                       float col_s) {
+    const bool row_ok = v < a.R;
+    float y[T];
+#pragma unroll
+    for (int j = 0; j < T; j += 4) {  // m0 a multiple of 4; texp has room for whole tiles
+        const int4 t = __ldcg(reinterpret_cast<const int4*>(a.texp + m0 + j));
+        y[j] = scale2(sum[j], row_e + t.x);
+        y[j + 1] = scale2(sum[j + 1], row_e + t.y);
+        y[j + 2] = scale2(sum[j + 2], row_e + t.z);
+        y[j + 3] = scale2(sum[j + 3], row_e + t.w);
+    }
+    if constexpr (MODE == kDx) {
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            if (row_ok && m0 + j < a.M) a.Y[(int64_t)(m0 + j) * a.R + v] = float_to_bf16_bits(y[j] * col_s);
+    } else if constexpr (MODE == kLinear) {
+        float res[T];
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            res[j] = a.ep.residual && row_ok && m0 + j < a.M ? load_bf16(a.ep.residual + (int64_t)(m0 + j) * a.R + v) : 0.f;
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            if (row_ok && m0 + j < a.M)
+                a.Y[(int64_t)(m0 + j) * a.R + v] = float_to_bf16_bits(linear_epilogue(y[j], a.ep, bias, res[j]));
+    } else {
+        const int p = v & 1;
+        const int64_t col = v >> 1;
+        if (a.ep.GU) {
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+                if (row_ok && m0 + j < a.M)
+                    a.ep.GU[(int64_t)(m0 + j) * 2 * a.I + p * a.I + col] = float_to_bf16_bits(y[j]);
+        }
+        // the even lane finishes the first half of the tokens, the odd lane the second
+#pragma unroll
+        for (int j = 0; j < T / 2; ++j) {
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, p ? y[j] : y[T / 2 + j], 1);
+            const float gate = p ? got : y[j], up = p ? y[T / 2 + j] : got;
+            const int m = m0 + (p ? T / 2 : 0) + j;
+            if (row_ok && m < a.M) a.Y[(int64_t)m * a.I + col] = float_to_bf16_bits(act_f(gate, a.ep.act) * up);
+        }
+    }
+}
+
+// The value of code q in FP16 where the zero point is beyond 1024.
+__device__ __noinline__ uint32_t far_value(uint32_t q, float s, int z, int e) {
+    const double v = (double)((long long)q - z) * s;
+    const double f = __longlong_as_double((long long)(1023 - e) << 52);  // 2^-e, |e| < 400
+    return __half_as_ushort(__double2half(v * f));
+}
+
+template <int MODE, int NT>
+__global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_constant__ CUtensorMap tx,
+                                                             const __grid_constant__ CUtensorMap tq, const HArgs a) {
+    using C = Cfg<NT>;
+    constexpr int S = C::kStages;
+    constexpr bool kBack = MODE == kDx;
+    constexpr uint32_t kIdesc = idesc_f16(kTileRows, NT, kBack);
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t full[S], afull[S], empty[S], mdone[2], dfree[2];
+    __shared__ __align__(8) uint64_t drained;
+    __shared__ uint32_t s_tmem;
+    const uint32_t raw = smem_u32(smem_raw);
+    unsigned char* ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // same offset in both CTAs
+
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int b = blockIdx.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&afull[s], kDqWarps * 2);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&mdone[i], 1);
+            mbar_init(&dfree[i], kEpiWarps * 2);
+        }
+        mbar_init(&drained, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    if (warp == 0) tmem_alloc_pair(&s_tmem, C::kTmemCols);
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    Segments seg(b, a);
+
+    if (warp == kTmaWarp) {  // ------------------------------------------------------------ TMA
+        if (lane == 0) {
+            prefetch_tmap(&tx);
+            prefetch_tmap(&tq);
+            pdl_wait_primary();  // operands and meta words come from the preparation kernels
+            int it = 0;
+            bool ok = true;
+            while (ok && seg.next(a)) {
+                int rt, mt;
+                tile_coords(seg.tile, a, rt, mt);
+                const int row0 = rt * kTileRows + rank * kBM;  // this CTA's first output row
+                for (int ks = seg.s0; ks < seg.s1; ++ks, ++it) {
+                    const int s = it % S;
+                    if (it >= S && !mbar_wait(&empty[s], ((it / S) - 1) & 1, a.fault, 171)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char* st = ring + s * C::kStageBytes;
+                    unsigned char *codes = st + C::kXBytes + kABytes, *meta = codes + kCodeBytes;
+                    if constexpr (!kBack) {  // one line of 128 rows per group in the 64 k
+                        const int lines = a.group == 32 ? 2 : 1;
+                        mbar_arrive_expect_tx(&full[s], C::kXBytes + kCodeBytes + lines * kBM * 4);
+                        if constexpr (MODE == kGated)
+                            tma_load_3d(codes, &tq, ks * (kBK / 8), 0, row0 / 2, &full[s]);
+                        else
+                            tma_load_2d(codes, &tq, ks * (kBK / 8), row0, &full[s]);
+                        const int g0 = ks * kBK / a.group;
+                        for (int l = 0; l < lines; ++l)
+                            bulk_load(meta + l * kBM * 4, a.meta + (int64_t)(g0 + l) * a.Rp + row0, kBM * 4, &full[s]);
+                    } else {  // one line of 64 weight rows per group in the CTA's 128 columns
+                        const int lines = kBM / a.group;
+                        mbar_arrive_expect_tx(&full[s], C::kXBytes + kCodeBytes + lines * kBK * 4);
+                        tma_load_2d(codes, &tq, row0 / 8, ks * kBK, &full[s]);
+                        for (int l = 0; l < lines; ++l)  // columns past K: any line (never stored)
+                            bulk_load(meta + l * kBK * 4,
+                                      a.meta + (int64_t)min(row0 / a.group + l, a.GQ - 1) * a.Rp + ks * kBK, kBK * 4,
+                                      &full[s]);
+                    }
+                    tma_load_2d(st, &tx, ks * kBK, mt * NT + rank * (NT / 2), &full[s]);
+                }
+            }
+            // copies in flight land before the CTA may exit
+            for (int i = max(0, it - S); i < it; ++i) mbar_wait(&full[i % S], (i / S) & 1, a.fault, 172);
+        }
+    } else if (warp == kMmaWarp) {  // ------------------------------------------------ MMA issue
+        if (lane == 0 && rank == 0) {
+            int it = 0, sc = 0;
+            bool ok = true;
+            while (ok && seg.next(a)) {
+                const int buf = sc & 1;
+                if (sc >= 2 && !mbar_wait(&dfree[buf], ((sc >> 1) - 1) & 1, a.fault, 173)) break;
+                for (int ks = seg.s0; ks < seg.s1; ++ks, ++it) {
+                    const int s = it % S;
+                    // the dequantisers of both CTAs waited on their copies first
+                    if (!mbar_wait(&afull[s], (it / S) & 1, a.fault, 174)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t xaddr = smem_u32(ring + s * C::kStageBytes), aaddr = xaddr + C::kXBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_ss_pair(tmem + buf * NT,
+                                     kBack ? sw128_mnmajor_desc(aaddr + kk * 2048) : sw128_kmajor_desc(aaddr + kk * 32),
+                                     sw128_kmajor_desc(xaddr + kk * 32), kIdesc, ks > seg.s0 || kk > 0);
+                    umma_commit_pair(&empty[s], 0x3);
+                }
+                if (ok) umma_commit_pair(&mdone[buf], 0x3);
+                ++sc;
+            }
+            umma_commit_pair(&drained, 0x1);  // every MMA issued completes before the teardown
+            mbar_wait(&drained, 0, a.fault, 175);
+        }
+    } else if (warp < kDqWarps) {  // ------------------------------------------------- dequantisers
+        // this thread's 4 code words: row (forward: output row; backward: contraction step) and 16-byte chunk c
+        const int tid = threadIdx.x;
+        const int row = kBack ? (warp >> 2) * 32 + lane : tid & 127;
+        const int c = kBack ? warp & 3 : tid >> 7;
+        const int code_off = kBack ? row * 64 + 16 * (c ^ ((row >> 1) & 3)) : row * 32 + 16 * (c ^ ((row >> 2) & 1));
+        const int line = kBack ? c * 32 / a.group : (a.group == 32 ? c : 0);
+        const int meta_off = (line * (kBack ? kBK : kBM) + row) * 4;
+        // operand rows of 128 bytes, chunk j at j ^ (row % 8); backward the second 64 columns 8 KB on
+        const int a_off = kBack ? (c >> 1) * 8192 + row * 128 : row * 128;
+        const int chunk0 = kBack ? (c & 1) * 4 : c * 4;
+        int it = 0;
+        bool ok = true;
+        while (ok && seg.next(a)) {
+            int rt, mt;
+            tile_coords(seg.tile, a, rt, mt);
+            for (int ks = seg.s0; ks < seg.s1; ++ks, ++it) {
+                const int s = it % S;
+                if (!mbar_wait(&full[s], (it / S) & 1, a.fault, 176)) {
+                    ok = false;
+                    break;
+                }
+                unsigned char* st = ring + s * C::kStageBytes;
+                unsigned char* arow = st + C::kXBytes + a_off;
+                const unsigned char* codes = st + C::kXBytes + kABytes;
+                const uint4 w4 = *reinterpret_cast<const uint4*>(codes + code_off);
+                const uint32_t mw = *reinterpret_cast<const uint32_t*>(codes + kCodeBytes + meta_off);
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                if ((mw >> 16) != 0x7FFFu) {
+                    const uint32_t sp = __byte_perm(mw, mw, 0x1010), zp = __byte_perm(mw, mw, 0x3232);
+                    const __half2 s2 = *reinterpret_cast<const __half2*>(&sp), z2 = *reinterpret_cast<const __half2*>(&zp);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t p;  // (1024 + q) of codes e and e + 4
+                            asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(p) : "r"(w[j] >> (4 * e)));
+                            const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&p), z2), s2);
+                            o[e] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        *reinterpret_cast<uint4*>(arow + 16 * ((chunk0 + j) ^ (row & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                } else {
+                    const int64_t vrow = kBack ? (int64_t)ks * kBK + row : (int64_t)rt * kTileRows + rank * kBM + row;
+                    const int64_t n = MODE == kGated ? gated_row(vrow, a.I) : vrow;
+                    const int g = kBack ? min((rt * kTileRows + rank * kBM + c * 32) / a.group, a.GQ - 1)
+                                        : (ks * kBK + c * 32) / a.group;
+                    const float sv = bf16_bits_to_float(__ldg(a.scales + n * a.GQ + g));
+                    const int z = __ldg(a.zeros + n * a.GQ + g), e2 = (int)(int16_t)(mw & 0xFFFFu);
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
+#pragma unroll 1
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = far_value((w[j] >> (4 * e)) & 15u, sv, z, e2) |
+                                   (far_value((w[j] >> (4 * e + 16)) & 15u, sv, z, e2) << 16);
+                        *reinterpret_cast<uint4*>(arow + 16 * ((chunk0 + j) ^ (row & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor core
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(&afull[s], 0);
+            }
+        }
+    } else {  // ------------------------------------------------------------------------- epilogue
+        pdl_wait_primary();  // exponents come from the preparation kernels, the residual from earlier ones
+        const int quad = warp & 3;
+        const int lrow = quad * 32 + lane;  // TMEM lane
+        // backward: position (0,1,..,7) of every 8-block holds column (0,4,1,5,2,6,3,7)
+        const int orow = kBack ? (lrow & ~7) | ((lrow & 7) >> 1) | ((lrow & 1) << 2) : lrow;
+        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+        int sc = 0;
+        bool ok = true;
+        while (seg.next(a)) {
+            int rt, mt;
+            tile_coords(seg.tile, a, rt, mt);
+            const int buf = sc & 1;
+            if (ok && !mbar_wait(&mdone[buf], (sc >> 1) & 1, a.fault, 177)) ok = false;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            ++sc;
+            if (!ok) continue;
+            tc_fence_after();
+            const bool whole = seg.s0 == 0 && seg.s1 == a.NS;
+            const int trow = rank * kBM + orow, v = rt * kTileRows + trow;
+            float* part = a.partial + (int64_t)slot_of(b, seg.s0) * NT * kTileRows + trow;
+            float bias = 0.f, col_s = 1.f;
+            int row_e = 0;
+            if (v < a.R) {
+                if constexpr (!kBack) row_e = __ldcg(a.exps + v);
+                if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
+                if (kBack && a.inv_s) col_s = __ldg(a.inv_s + v);
+            }
+            constexpr int T = 16;
+#pragma unroll 1
+            for (int c0 = 0; c0 < NT; c0 += T) {
+                uint32_t d[T];
+                tmem_ld16(tl + buf * NT + c0, d);
+                tmem_wait_ld();
+                if (c0 + T == NT) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(&dfree[buf], 0);
+                }
+                if (whole) {
+                    float sum[T];
+#pragma unroll
+                    for (int j = 0; j < T; ++j) sum[j] = __uint_as_float(d[j]);
+                    if (mt * NT + c0 < a.M) finish<MODE, T>(a, sum, mt * NT + c0, v, bias, row_e, col_s);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < T; ++j) part[(int64_t)(c0 + j) * kTileRows] = __uint_as_float(d[j]);
+                }
+            }
+        }
+    }
+    // teardown: every role done, every MMA complete (drained), no arrival still bound for the peer
+    __syncwarp();
+    cluster_sync();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, C::kTmemCols);
+    }
+}
+
+// The cut tiles: adds each tile's parts in cluster order and finishes the outputs.  One block per tile and 8
+// tokens, a thread per row of the tile.
+template <int MODE, int NT>
+__global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
+    constexpr int T = 8;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const int r = blockIdx.x / (NT / T), c0 = (blockIdx.x - r * (NT / T)) * T;
+    int rt, mt;
+    tile_coords(a.whole_tiles + r, a, rt, mt);
+    if (mt * NT + c0 >= a.M) return;
+    const int first = cta_of_unit((int64_t)r * a.NS, a.base, a.rem);
+    const int last = cta_of_unit((int64_t)r * a.NS + a.NS - 1, a.base, a.rem);
+    if (first == last) return;  // one cluster ran the tile whole
+    const int v = rt * kTileRows + threadIdx.x;
+    float sum[T];
+#pragma unroll
+    for (int j = 0; j < T; ++j) sum[j] = 0.f;
+    for (int b = first; b <= last; ++b) {
+        const int64_t u = (int64_t)b * a.base + min(b, a.rem);  // the cluster's first stage
+        const int s0 = (int)max(u - (int64_t)r * a.NS, (int64_t)0);
+        const float* p = a.partial + ((int64_t)slot_of(b, s0) * NT + c0) * kTileRows + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < T; ++j) sum[j] += __ldcg(p + j * kTileRows);
+    }
+    float bias = 0.f, col_s = 1.f;
+    int row_e = 0;
+    if (v < a.R) {
+        if (MODE != kDx) row_e = __ldcg(a.exps + v);
+        if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
+        if (MODE == kDx && a.inv_s) col_s = __ldg(a.inv_s + v);
+    }
+    finish<MODE, T>(a, sum, mt * NT + c0, v, bias, row_e, col_s);
+}
+
+// ------------------------------------------------------------------ host
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Tokens per tile.
+int tile_tokens(int64_t M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+struct Layout {
+    int64_t Rp, Cp, Mp;
+    size_t meta, exps, texp, op, partial, total;  // byte offsets after the counter area
+};
+
+Layout layout_h(int64_t M, int64_t N, int64_t K, int group, bool back, int num_sms) {
+    Layout l{};
+    const int NT = tile_tokens(M);
+    l.Rp = (N + 255) / 256 * 256;
+    l.Cp = back ? (N + 63) / 64 * 64 : K;
+    l.Mp = (M + 255) / 256 * 256;
+    size_t o = kCounterBytes;
+    l.meta = o;
+    o += up256((size_t)(K / group) * l.Rp * 4);
+    l.exps = o;
+    o += up256((size_t)l.Rp * 4);
+    l.texp = o;
+    o += up256((size_t)l.Mp * 4);
+    l.op = o;
+    o += up256((size_t)M * l.Cp * 2);
+    l.partial = o;
+    o += (size_t)(num_sms / 2) * 2 * NT * kTileRows * 4;
+    l.total = o;
+    return l;
+}
+
+template <class Kern, class... Args>
+int launch_pdl(Kern kernel, int64_t grid, int block, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
+}
+
+template <int MODE, int NT>
+int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, cudaStream_t stream) {
+    using C = Cfg<NT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = 2;
+    attrs[0].val.clusterDim.y = 1;
+    attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 1;
+    // clusters that are resident at once (a cluster needs two free SMs of one GPC)
+    static PerContext<int> cache;
+    const int units = cache.get([&]() -> int {
+        if (cudaFuncSetAttribute(gemm_h_kernel<MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
+            cudaSuccess)
+            return 0;
+        cudaLaunchConfig_t q = cfg;
+        q.gridDim = dim3((unsigned)(num_sms_current() / 2 * 2));
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, gemm_h_kernel<MODE, NT>, &q) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        return n < num_sms_current() / 2 ? n : num_sms_current() / 2;
+    });
+    if (units <= 0) return W4A16_ERR_CUDA;
+    cfg.numAttrs = 2;
+    const int tiles = a.m_tiles * a.r_tiles;
+    // whole waves run whole; a last wave that fills at least nine tenths of the clusters too
+    int cut = tiles % units;
+    if (cut * 10 >= units * 9) cut = 0;
+    a.whole_tiles = tiles - cut;
+    a.units = units;
+    a.base = 1;
+    a.rem = 0;
+    a.split_units = 0;
+    if (cut > 0) {
+        const int64_t stages = (int64_t)cut * a.NS;
+        int64_t parts = stages / 4;  // at least four stages each
+        if (parts > units) parts = units;
+        if (parts < 1) parts = 1;
+        a.split_units = (int)parts;
+        a.base = (int)(stages / parts);
+        a.rem = (int)(stages % parts);
+    }
+    const int busy = a.whole_tiles > 0 ? (a.whole_tiles < units ? a.whole_tiles : units) : 0;
+    const int grid = busy > a.split_units ? busy : a.split_units;
+    cfg.gridDim = dim3((unsigned)(grid * 2));
+    if (cudaLaunchKernelEx(&cfg, gemm_h_kernel<MODE, NT>, tx, tq, a) != cudaSuccess) return W4A16_ERR_CUDA;
+    if (cut == 0) return W4A16_OK;
+    return launch_pdl(gemm_h_join_kernel<MODE, NT>, (int64_t)cut * (NT / 8), kTileRows, stream, a);
+}
+
+template <int MODE>
+int launch_mode(int NT, const HArgs& a, const CUtensorMap& tx, const CUtensorMap& tq, cudaStream_t stream) {
+    return NT == 64    ? launch_tiles<MODE, 64>(a, tx, tq, stream)
+           : NT == 128 ? launch_tiles<MODE, 128>(a, tx, tq, stream)
+                       : launch_tiles<MODE, 256>(a, tx, tq, stream);
+}
+
+}  // namespace
+
+size_t gemm_h_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, bool backward, int num_sms) {
+    return layout_h(M, N, K, group, backward, num_sms).total;
+}
+
+int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, int group, const uint32_t* qweight,
+                  const uint16_t* scales, const int32_t* zeros, int64_t N, const FusedEpilogue& e, uint16_t* Y,
+                  void* workspace, cudaStream_t stream) {
+    const Layout l = layout_h(M, N, K, group, false, num_sms_current());
+    const int NT = tile_tokens(M);
+    char* ws = reinterpret_cast<char*>(workspace);
+    int* fault = fault_word();
+    if (!fault) return W4A16_ERR_CUDA;
+    const int64_t I = e.gated ? N / 2 : 0;
+    HArgs a{};
+    a.meta = reinterpret_cast<uint32_t*>(ws + l.meta);
+    a.exps = reinterpret_cast<int*>(ws + l.exps);
+    a.texp = reinterpret_cast<int*>(ws + l.texp);
+    a.scales = scales;
+    a.zeros = zeros;
+    a.Y = Y;
+    a.partial = reinterpret_cast<float*>(ws + l.partial);
+    a.fault = fault;
+    a.ep = e;
+    a.I = I;
+    a.M = (int)M;
+    a.R = (int)N;
+    a.C = (int)K;
+    a.Rp = (int)l.Rp;
+    a.GQ = (int)(K / group);
+    a.group = group;
+    a.N = (int)N;
+    a.NS = (int)(K / kBK);
+    a.m_tiles = (int)ceil_div(M, NT);
+    a.r_tiles = (int)ceil_div(N, kTileRows);
+    CUtensorMap tx, tq;
+    if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + l.op, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kBK,
+                        (uint32_t)NT / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4A16_ERR_CUDA;
+    const bool ok = e.gated ? encode_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight,
+                                             {(uint64_t)K / 8, 2, (uint64_t)I}, {(uint64_t)I * K / 2, (uint64_t)K / 2},
+                                             {kBK / 8, 2, kBM / 2}, CU_TENSOR_MAP_SWIZZLE_32B)
+                            : encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N,
+                                             (uint64_t)K / 2, kBK / 8, kBM, CU_TENSOR_MAP_SWIZZLE_32B);
+    if (!ok) return W4A16_ERR_CUDA;
+    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int*>(ws + l.exps),
+                      (int)N, (int)l.Rp, a.GQ, I};
+    const TokenArgs t{X, xscale, reinterpret_cast<__half*>(ws + l.op), reinterpret_cast<int*>(ws + l.texp), (int)M,
+                      (int)K};
+    const int meta_blocks = (int)(l.Rp / kMetaRows);
+    const int st = launch_pdl(prep_forward_kernel, meta_blocks + M, kPrepThreads, stream, ma, meta_blocks, t);
+    if (st != W4A16_OK) return st;
+    return e.gated ? launch_mode<kGated>(NT, a, tx, tq, stream) : launch_mode<kLinear>(NT, a, tx, tq, stream);
+}
+
+int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU, int act, uint16_t* dGU, int64_t M,
+                     int64_t N, int group, const uint32_t* qweight, const uint16_t* scales, const int32_t* zeros,
+                     int64_t K, const float* inv_s, uint16_t* dX, void* workspace, cudaStream_t stream) {
+    const Layout l = layout_h(M, N, K, group, true, num_sms_current());
+    const int NT = tile_tokens(M);
+    char* ws = reinterpret_cast<char*>(workspace);
+    int* fault = fault_word();
+    if (!fault) return W4A16_ERR_CUDA;
+    HArgs a{};
+    a.meta = reinterpret_cast<uint32_t*>(ws + l.meta);
+    a.exps = reinterpret_cast<int*>(ws + l.exps);
+    a.texp = reinterpret_cast<int*>(ws + l.texp);
+    a.scales = scales;
+    a.zeros = zeros;
+    a.inv_s = inv_s;
+    a.Y = dX;
+    a.partial = reinterpret_cast<float*>(ws + l.partial);
+    a.fault = fault;
+    a.M = (int)M;
+    a.R = (int)K;
+    a.C = (int)N;
+    a.Rp = (int)l.Rp;
+    a.GQ = (int)(K / group);
+    a.group = group;
+    a.N = (int)N;
+    a.NS = (int)ceil_div(N, kBK);
+    a.m_tiles = (int)ceil_div(M, NT);
+    a.r_tiles = (int)ceil_div(K, kTileRows);
+    CUtensorMap tx, tq;
+    // rows of N values, Np apart: what lies past N is filled with zeros
+    if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + l.op, (uint64_t)N, (uint64_t)M, (uint64_t)l.Cp * 2,
+                        kBK, (uint32_t)NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N, (uint64_t)K / 2,
+                        kBM / 8, kBK, CU_TENSOR_MAP_SWIZZLE_64B))
+        return W4A16_ERR_CUDA;
+    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int*>(ws + l.exps),
+                      (int)N, (int)l.Rp, a.GQ, 0};
+    int st = launch_pdl(prep_meta_kernel, l.Rp / kMetaRows, kPrepThreads, stream, ma);
+    if (st != W4A16_OK) return st;
+    GradArgs g{};
+    g.dY = dY;
+    g.dH = dH;
+    g.GU = GU;
+    g.dGU = dGU;
+    g.exps = a.exps;
+    g.Dh = reinterpret_cast<__half*>(ws + l.op);
+    g.texp = reinterpret_cast<int*>(ws + l.texp);
+    g.N = (int)N;
+    g.I = (int)(N / 2);
+    g.act = act;
+    g.Np = l.Cp;
+    // 16-byte loads where every row (gated: every half row) of the inputs starts on a 16-byte boundary
+    if (dH)
+        st = g.I % 8 == 0 ? launch_pdl(prep_grad_kernel<8, true>, M, kGradThreads, stream, g)
+                          : launch_pdl(prep_grad_kernel<1, true>, M, kGradThreads, stream, g);
+    else
+        st = N % 8 == 0 ? launch_pdl(prep_grad_kernel<8, false>, M, kGradThreads, stream, g)
+                        : launch_pdl(prep_grad_kernel<1, false>, M, kGradThreads, stream, g);
+    if (st != W4A16_OK) return st;
+    return launch_mode<kDx>(NT, a, tx, tq, stream);
+}
+
+}  // namespace w4a16

@@ -39,6 +39,7 @@
 // partials are summed in a fixed order.
 #include "common.cuh"
 #include "decode_units.cuh"
+#include "epilogue.cuh"
 #include "sm100.cuh"
 
 #include <mutex>
@@ -1280,7 +1281,7 @@ namespace {
 // slots, so the call is one launch (two with the prescale).
 int launch_cc_path(const uint16_t* X, const float* xscale, int64_t K, const uint32_t* qweight, const uint16_t* scales,
                    const int32_t* zeros, int64_t N, uint16_t* Y, void* workspace, const DecodePlan& plan,
-                   cudaStream_t stream, const uint16_t* X_host, uint16_t* Y_host) {
+                   cudaStream_t stream, const uint16_t* X_host, uint16_t* Y_host, const FusedEpilogue* ep) {
     const int G = (int)(K / kGroup);
     CUtensorMap tq, tsc, tze;
     if (!cached_tmap(0, qweight, N, K / 8, &tq) || !cached_tmap(2, scales, N, G, &tsc) ||
@@ -1339,6 +1340,8 @@ int launch_cc_path(const uint16_t* X, const float* xscale, int64_t K, const uint
     args.row_tiles = plan.row_tiles;
     const int st = launch_cc(tq, tsc, tze, args, plan.grid, stream);
     if (st != W4A16_OK) return st;
+    if (ep)
+        return launch_cc_epilogue(args.partial, *ep, Y, N, plan.cc_cpt, plan.row_tiles, plan.cc_tiles_a, G / 2, stream);
     return launch_cc_reduce(args.partial, Y, N, plan.cc_cpt, plan.row_tiles, stream, Y_host, plan.cc_tiles_a,
                             G / 2);
 }
@@ -1371,15 +1374,17 @@ int launch_cc_reduce(const float* partial, uint16_t* Y, int64_t N, int cpt, int 
 
 int launch_decode(const uint16_t* X, const float* xscale, int64_t M, int64_t K, const uint32_t* qweight,
                   const uint16_t* scales, const int32_t* zeros, int64_t N, uint16_t* Y, void* workspace,
-                  const DecodePlan& plan, cudaStream_t stream, const uint16_t* X_host, uint16_t* Y_host) {
+                  const DecodePlan& plan, cudaStream_t stream, const uint16_t* X_host, uint16_t* Y_host,
+                  const FusedEpilogue* ep) {
+    if (ep && !plan.mt && !plan.cc_tokens) return W4A16_ERR_ARG;  // those GEMVs leave every sum in slots
     if (plan.mt)
         return launch_decode_mt(X, xscale, M, K, qweight, scales, zeros, N, Y,
-                                reinterpret_cast<char*>(workspace) + plan.ws_counter_bytes, stream);
+                                reinterpret_cast<char*>(workspace) + plan.ws_counter_bytes, stream, ep);
     if (plan.bf)
         return launch_decode_bf(X, xscale, M, K, kGroup, qweight, scales, zeros, N, Y,
                                 reinterpret_cast<char*>(workspace) + plan.ws_counter_bytes, stream);
     if (plan.cc_tokens)
-        return launch_cc_path(X, xscale, K, qweight, scales, zeros, N, Y, workspace, plan, stream, X_host, Y_host);
+        return launch_cc_path(X, xscale, K, qweight, scales, zeros, N, Y, workspace, plan, stream, X_host, Y_host, ep);
     if (X_host || Y_host) return W4A16_ERR_ARG;  // host-mapped transfers are the one-token path's
     CUtensorMap tq;
     if (!cached_tmap(0, qweight, N, K / 8, &tq)) return W4A16_ERR_CUDA;

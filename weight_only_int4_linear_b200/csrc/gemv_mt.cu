@@ -30,6 +30,7 @@
 // the unit's codes (after the dependent-launch wait; the codes first).
 #include "common.cuh"
 #include "decode_units.cuh"
+#include "epilogue.cuh"
 #include "sm100.cuh"
 
 namespace w4a16 {
@@ -95,6 +96,7 @@ struct MtArgs {
     int M, N, G;
     int units_base, units_rem;
     int max_slots;
+    int slots_only;  // nonzero: every row tile leaves through its slots (a fused epilogue adds them)
 };
 
 // One warp per (group g, token m < NT): the digit rows of token m (zero for m >= M) and its
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_mt_kernel(const __grid_con
     auto flush = [&](int tile) {
         const int first = cta_of_unit((int64_t)tile * G, a.units_base, a.units_rem);
         const int last = cta_of_unit((int64_t)tile * G + G - 1, a.units_base, a.units_rem);
-        if (first == last) {
+        if (first == last && !a.slots_only) {
 #pragma unroll
             for (int q = 0; q < TPL; ++q) {
                 const int m = mt_token<NT>(tig, q);
@@ -496,7 +498,8 @@ size_t mt_workspace_bytes(int64_t M, int64_t N, int64_t K, int num_sms) {
 
 int launch_decode_mt(const uint16_t* X, const float* xscale, int64_t M, int64_t K, const uint32_t* qweight,
                      const uint16_t* scales, const int32_t* zeros, int64_t N, uint16_t* Y, void* scratch,
-                     cudaStream_t stream) {
+                     cudaStream_t stream, const FusedEpilogue* ep) {
+    if (ep && M > 16) return W4A16_ERR_ARG;
     const int G = (int)(K / kGroup);
     CUtensorMap tq, tsc, tze;
     if (!tmap_2d_cached(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N, (uint64_t)K / 2,
@@ -534,10 +537,17 @@ int launch_decode_mt(const uint16_t* X, const float* xscale, int64_t M, int64_t 
         args.units_base = p.units_base;
         args.units_rem = p.units_rem;
         args.max_slots = p.max_slots;
+        args.slots_only = ep != nullptr;
         st = nt == 4   ? launch_mt_kernel<4>(tq, tsc, tze, args, p.grid, stream)
              : nt == 8 ? launch_mt_kernel<8>(tq, tsc, tze, args, p.grid, stream)
                        : launch_mt_kernel<16>(tq, tsc, tze, args, p.grid, stream);
         if (st != W4A16_OK) return st;
+        if (ep) {  // M <= 16: one launch takes all tokens
+            st = launch_deal_epilogue(partial, *ep, Y, N, Mc, G, p.units_base, p.units_rem, p.max_slots, p.row_tiles,
+                                      stream);
+            if (st != W4A16_OK) return st;
+            continue;
+        }
         st = launch_decode_reduce(partial, args.Y, N, Mc, G, p.units_base, p.units_rem, p.max_slots, p.row_tiles,
                                   stream);
         if (st != W4A16_OK) return st;

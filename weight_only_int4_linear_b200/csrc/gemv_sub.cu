@@ -7,6 +7,7 @@
 // the per-lane folds and the 4-unit metadata blocks (described at SubCfg).
 #include "common.cuh"
 #include "decode_units.cuh"
+#include "epilogue.cuh"
 #include "sm100.cuh"
 
 #include <mutex>
@@ -435,7 +436,8 @@ size_t decode_sub_workspace_bytes(int64_t N, int64_t K, int group) {
 
 int launch_decode_sub(const uint16_t* X, int64_t M, int64_t K, int group, const uint32_t* qweight,
                       const uint16_t* scales, const int32_t* zeros, int64_t N, uint16_t* Y, void* workspace,
-                      cudaStream_t stream) {
+                      cudaStream_t stream, const FusedEpilogue* ep) {
+    if (ep && M != 1) return W4A16_ERR_ARG;
     const DecodePlan plan = plan_decode_sub(N, K, group, num_sms_current());
     const int ng = (int)(K / group);
     CUtensorMap tq, tsc, tze;
@@ -460,7 +462,8 @@ int launch_decode_sub(const uint16_t* X, int64_t M, int64_t K, int group, const 
         int st = group == 64 ? launch_sub<64>(tq, tsc, tze, args, plan.grid, stream)
                              : launch_sub<32>(tq, tsc, tze, args, plan.grid, stream);
         if (st != W4A16_OK) return st;
-        st = launch_cc_reduce(args.partial, Y + m * N, N, plan.cc_cpt, plan.row_tiles, stream);
+        st = ep ? launch_cc_epilogue(args.partial, *ep, Y, N, plan.cc_cpt, plan.row_tiles, -1, 0, stream)
+                : launch_cc_reduce(args.partial, Y + m * N, N, plan.cc_cpt, plan.row_tiles, stream);
         if (st != W4A16_OK) return st;
     }
     return W4A16_OK;

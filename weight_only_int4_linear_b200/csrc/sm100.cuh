@@ -301,6 +301,10 @@ bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 
+// The same for a 3-D tensor: dims[0] innermost and dense, strides (bytes) of dims 1 and 2 in any order.
+bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[3],
+                    const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
+
 // A 2-D tensor map as encode_tmap_2d makes it, encoded once per (base, shape, type, box, swizzle)
 // and kept in a process-wide cache (the map describes global addresses only, so it stays valid for
 // any context in which the base address is).  Returns false on failure.
