@@ -22,9 +22,9 @@
 // Tile: 256 output rows (weight rows, or K columns backward) x NT tokens by a
 // cluster of two CTAs with the pair MMA (M = 256); each CTA dequantises its 128
 // rows and holds half of the tile's tokens.  Stages of 64 along the contraction.
-// Forward, a thread's 4 code words are 32 consecutive k of one row: the K-major
+// Forward, a thread's 8 code words are 64 consecutive k of one row: the K-major
 // operand (K order (0,4,1,5,2,6,3,7) in every 8-block, which the token operand
-// is prepared in).  Backward, the same words are 32 consecutive output rows of
+// is prepared in).  Backward, the same words are 64 consecutive output rows of
 // one contraction step: the MN-major operand, its rows in that order, which the
 // epilogue undoes in its addresses.
 //
@@ -37,8 +37,10 @@
 // tensor map, row 2 j + p = row p I + j, so that a pair of neighbouring lanes
 // holds both sums of an output.
 //
-// Warps (448 threads): 0-7 dequantise, 8-11 epilogue (TMEM lane quadrants), 12
-// TMA, 13 MMA issue (rank 0).  Two accumulators: a tile's epilogue overlaps the
+// Warps: three groups of four dequantiser warps, which take the stages in turn (a
+// stage's dequantisation is a chain of waits -- copy, loads, stores, proxy fence --
+// longer than its MMAs), four epilogue warps (TMEM lane quadrants), TMA, MMA issue
+// (rank 0).  Two accumulators: a tile's epilogue overlaps the
 // next tile's MMAs.
 #include "decode_units.cuh"
 #include "epilogue.cuh"
@@ -55,9 +57,13 @@ constexpr int kBK = 64;                        // contraction per stage
 constexpr int kABytes = kBM * kBK * 2;         // 16 KB
 constexpr int kCodeBytes = kBM * kBK / 2;      // 4 KB
 constexpr int kMetaBytes = 1024;               // up to 8 lines of 128 B x ... (see meta words below)
-constexpr int kDqWarps = 8, kEpiWarps = 4;
+#ifndef W4A16_H_DQ_GROUPS
+#define W4A16_H_DQ_GROUPS 3
+#endif
+constexpr int kDqGroups = W4A16_H_DQ_GROUPS;   // groups of 4 dequantiser warps, each taking every kDqGroups-th stage
+constexpr int kDqWarps = 4 * kDqGroups, kEpiWarps = 4;
 constexpr int kTmaWarp = kDqWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * 32;  // 448
+constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kTopExp = 15;                    // scaled operands stay below 2^15
 
 enum Mode { kLinear = 0, kGated = 1, kDx = 2 };
@@ -464,6 +470,24 @@ struct Segments {
         return true;
     }
 };
+// Position in the ring of S stages: stage s, whose barriers complete the phase of this parity on this round.
+template <int S>
+struct Ring {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == S) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void prev() {
+        if (s-- == 0) {
+            s = S - 1;
+            parity ^= 1u;
+        }
+    }
+};
 // Slot of cluster b's part of a cut tile that starts at stage s0: a cluster's range has at most one part that
 // starts inside a tile (its first) and one that starts a tile and does not end it (its last).
 __device__ __forceinline__ int slot_of(int b, int s0) { return 2 * b + (s0 == 0 ? 1 : 0); }
@@ -516,11 +540,19 @@ __device__ __forceinline__ void finish(const HArgs& a, float (&sum)[T], int m0, 
     }
 }
 
-// The value of code q in FP16 where the zero point is beyond 1024.
-__device__ __noinline__ uint32_t far_value(uint32_t q, float s, int z, int e) {
-    const double v = (double)((long long)q - z) * s;
-    const double f = __longlong_as_double((long long)(1023 - e) << 52);  // 2^-e, |e| < 400
-    return __half_as_ushort(__double2half(v * f));
+// 32 values whose zero point is beyond 1024, from their 4 code words, in binary64: chunks j0 .. j0 + 3 of arow.
+__device__ __noinline__ void far_half(unsigned char* arow, const unsigned char* codes, int j0, int x, float s, int z,
+                                      int e) {
+    const double f = __longlong_as_double((long long)(1023 - e) << 52) * s;  // s 2^-e, |e| < 400
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[j];
+        uint32_t* out = reinterpret_cast<uint32_t*>(arow + 16 * ((j0 + j) ^ x));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = __half_as_ushort(__double2half((double)((long long)((w >> (4 * i)) & 15u) - z) * f));
+            const uint32_t hi = __half_as_ushort(__double2half((double)((long long)((w >> (4 * i + 16)) & 15u) - z) * f));
+            out[i] = lo | (hi << 16);
+        }
+    }
 }
 
 template <int MODE, int NT>
@@ -545,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&afull[s], kDqWarps * 2);
+            mbar_init(&afull[s], 4 * 2);  // one dequantiser group in each CTA
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -567,67 +599,74 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
             prefetch_tmap(&tx);
             prefetch_tmap(&tq);
             pdl_wait_primary();  // operands and meta words come from the preparation kernels
-            int it = 0;
+            Ring<S> r;
+            int issued = 0;
             bool ok = true;
+            const int lg = a.group >> 6;  // log2(group / 32): 0, 1, 2
+            const int lines = kBack ? kBM / a.group : (lg == 0 ? 2 : 1);
+            const uint32_t line_bytes = (kBack ? kBK : kBM) * 4;
+            const uint32_t bytes = C::kXBytes + kCodeBytes + lines * line_bytes;
             while (ok && seg.next(a)) {
                 int rt, mt;
                 tile_coords(seg.tile, a, rt, mt);
                 const int row0 = rt * kTileRows + rank * kBM;  // this CTA's first output row
-                for (int ks = seg.s0; ks < seg.s1; ++ks, ++it) {
-                    const int s = it % S;
-                    if (it >= S && !mbar_wait(&empty[s], ((it / S) - 1) & 1, a.fault, 171)) {
+                const int tok0 = mt * NT + rank * (NT / 2);
+                // backward: groups of the CTA's columns; columns past K take any line (never stored)
+                const int gb = min(row0 >> (5 + lg), a.GQ - lines);
+                for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
+                    if (!mbar_wait(&empty[r.s], r.parity ^ 1u, a.fault, 171)) {
                         ok = false;
                         break;
                     }
-                    unsigned char* st = ring + s * C::kStageBytes;
+                    uint64_t* bar = &full[r.s];
+                    unsigned char* st = ring + r.s * C::kStageBytes;
                     unsigned char *codes = st + C::kXBytes + kABytes, *meta = codes + kCodeBytes;
-                    if constexpr (!kBack) {  // one line of 128 rows per group in the 64 k
-                        const int lines = a.group == 32 ? 2 : 1;
-                        mbar_arrive_expect_tx(&full[s], C::kXBytes + kCodeBytes + lines * kBM * 4);
-                        if constexpr (MODE == kGated)
-                            tma_load_3d(codes, &tq, ks * (kBK / 8), 0, row0 / 2, &full[s]);
-                        else
-                            tma_load_2d(codes, &tq, ks * (kBK / 8), row0, &full[s]);
-                        const int g0 = ks * kBK / a.group;
-                        for (int l = 0; l < lines; ++l)
-                            bulk_load(meta + l * kBM * 4, a.meta + (int64_t)(g0 + l) * a.Rp + row0, kBM * 4, &full[s]);
-                    } else {  // one line of 64 weight rows per group in the CTA's 128 columns
-                        const int lines = kBM / a.group;
-                        mbar_arrive_expect_tx(&full[s], C::kXBytes + kCodeBytes + lines * kBK * 4);
-                        tma_load_2d(codes, &tq, row0 / 8, ks * kBK, &full[s]);
-                        for (int l = 0; l < lines; ++l)  // columns past K: any line (never stored)
-                            bulk_load(meta + l * kBK * 4,
-                                      a.meta + (int64_t)min(row0 / a.group + l, a.GQ - 1) * a.Rp + ks * kBK, kBK * 4,
-                                      &full[s]);
-                    }
-                    tma_load_2d(st, &tx, ks * kBK, mt * NT + rank * (NT / 2), &full[s]);
+                    mbar_arrive_expect_tx(bar, bytes);
+                    tma_load_2d(st, &tx, ks * kBK, tok0, bar);
+                    if constexpr (kBack)  // 64 weight rows x 128 columns
+                        tma_load_2d(codes, &tq, row0 / 8, ks * kBK, bar);
+                    else if constexpr (MODE == kGated)
+                        tma_load_3d(codes, &tq, ks * (kBK / 8), 0, row0 / 2, bar);
+                    else
+                        tma_load_2d(codes, &tq, ks * (kBK / 8), row0, bar);
+                    // one line of meta words per group: forward 128 rows, backward 64
+                    const uint32_t* mp = kBack ? a.meta + (int64_t)gb * a.Rp + ks * kBK
+                                               : a.meta + (int64_t)(2 * ks >> lg) * a.Rp + row0;
+                    for (int l = 0; l < lines; ++l)
+                        bulk_load(meta + l * line_bytes, mp + (int64_t)l * a.Rp, line_bytes, bar);
+                    ++issued;
                 }
             }
-            // copies in flight land before the CTA may exit
-            for (int i = max(0, it - S); i < it; ++i) mbar_wait(&full[i % S], (i / S) & 1, a.fault, 172);
+            // copies in flight land before the CTA may exit: the last S stages issued
+            for (int i = 0; i < min(issued, S); ++i) {
+                r.prev();
+                mbar_wait(&full[r.s], r.parity, a.fault, 172);
+            }
         }
     } else if (warp == kMmaWarp) {  // ------------------------------------------------ MMA issue
         if (lane == 0 && rank == 0) {
-            int it = 0, sc = 0;
+            Ring<S> r;
+            int sc = 0;
             bool ok = true;
+            const uint32_t x0 = smem_u32(ring), a0 = x0 + C::kXBytes;
+            const uint64_t xdesc = sw128_kmajor_desc(x0), adesc = kBack ? sw128_mnmajor_desc(a0) : sw128_kmajor_desc(a0);
+            constexpr uint64_t kAStep = (kBack ? 2048 : 32) >> 4, kXStep = 32 >> 4;  // descriptor units of 16 bytes
             while (ok && seg.next(a)) {
                 const int buf = sc & 1;
                 if (sc >= 2 && !mbar_wait(&dfree[buf], ((sc >> 1) - 1) & 1, a.fault, 173)) break;
-                for (int ks = seg.s0; ks < seg.s1; ++ks, ++it) {
-                    const int s = it % S;
+                for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
                     // the dequantisers of both CTAs waited on their copies first
-                    if (!mbar_wait(&afull[s], (it / S) & 1, a.fault, 174)) {
+                    if (!mbar_wait(&afull[r.s], r.parity, a.fault, 174)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t xaddr = smem_u32(ring + s * C::kStageBytes), aaddr = xaddr + C::kXBytes;
+                    const uint64_t off = (uint64_t)(r.s * (C::kStageBytes >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_ss_pair(tmem + buf * NT,
-                                     kBack ? sw128_mnmajor_desc(aaddr + kk * 2048) : sw128_kmajor_desc(aaddr + kk * 32),
-                                     sw128_kmajor_desc(xaddr + kk * 32), kIdesc, ks > seg.s0 || kk > 0);
-                    umma_commit_pair(&empty[s], 0x3);
+                        umma_ss_pair(tmem + buf * NT, adesc + off + kk * kAStep, xdesc + off + kk * kXStep, kIdesc,
+                                     ks > seg.s0 || kk > 0);
+                    umma_commit_pair(&empty[r.s], 0x3);
                 }
                 if (ok) umma_commit_pair(&mdone[buf], 0x3);
                 ++sc;
@@ -636,38 +675,48 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
             mbar_wait(&drained, 0, a.fault, 175);
         }
     } else if (warp < kDqWarps) {  // ------------------------------------------------- dequantisers
-        // this thread's 4 code words: row (forward: output row; backward: contraction step) and 16-byte chunk c
-        const int tid = threadIdx.x;
-        const int row = kBack ? (warp >> 2) * 32 + lane : tid & 127;
-        const int c = kBack ? warp & 3 : tid >> 7;
-        const int code_off = kBack ? row * 64 + 16 * (c ^ ((row >> 1) & 3)) : row * 32 + 16 * (c ^ ((row >> 2) & 1));
-        const int line = kBack ? c * 32 / a.group : (a.group == 32 ? c : 0);
-        const int meta_off = (line * (kBack ? kBK : kBM) + row) * 4;
-        // operand rows of 128 bytes, chunk j at j ^ (row % 8); backward the second 64 columns 8 KB on
-        const int a_off = kBack ? (c >> 1) * 8192 + row * 128 : row * 128;
-        const int chunk0 = kBack ? (c & 1) * 4 : c * 4;
-        int it = 0;
+        // Group dg takes every kDqGroups-th stage, a thread 8 of its code words: forward, 64 k of output row `row`;
+        // backward, 64 columns (half h of the CTA's) of contraction step `row`.
+        const int dg = warp >> 2, tid = threadIdx.x & 127;
+        const int row = kBack ? tid & 63 : tid, h = kBack ? tid >> 6 : 0;
+        // code chunks (16 bytes) of the row: forward 2, 32-byte swizzle; backward 4, this thread's 2 h and 2 h + 1,
+        // 64-byte swizzle
+        const int code0 = kBack ? row * 64 + 16 * ((2 * h) ^ ((row >> 1) & 3)) : row * 32 + 16 * ((row >> 2) & 1);
+        const int code1 = kBack ? row * 64 + 16 * ((2 * h + 1) ^ ((row >> 1) & 3)) : row * 32 + 16 * (((row >> 2) & 1) ^ 1);
+        // meta words of the thread's first and second 32 values
+        constexpr int kLine = kBack ? kBK : kBM;
+        const int lg = a.group >> 6;  // log2(group / 32)
+        const int meta0 = ((kBack ? 2 * h >> lg : 0) * kLine + row) * 4;
+        const int meta1 = ((kBack ? 2 * h + 1 >> lg : (lg == 0 ? 1 : 0)) * kLine + row) * 4;
+        const int a_off = h * 8192 + row * 128;  // operand row of 128 bytes, chunk j at j ^ (row % 8)
+        Ring<S> r;
+        int turn = dg;  // stages until this group's next
         bool ok = true;
         while (ok && seg.next(a)) {
             int rt, mt;
             tile_coords(seg.tile, a, rt, mt);
-            for (int ks = seg.s0; ks < seg.s1; ++ks, ++it) {
-                const int s = it % S;
-                if (!mbar_wait(&full[s], (it / S) & 1, a.fault, 176)) {
+            for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
+                if (turn-- != 0) continue;
+                turn = kDqGroups - 1;
+                const int s = r.s;
+                if (!mbar_wait(&full[s], r.parity, a.fault, 176)) {
                     ok = false;
                     break;
                 }
                 unsigned char* st = ring + s * C::kStageBytes;
                 unsigned char* arow = st + C::kXBytes + a_off;
                 const unsigned char* codes = st + C::kXBytes + kABytes;
-                const uint4 w4 = *reinterpret_cast<const uint4*>(codes + code_off);
-                const uint32_t mw = *reinterpret_cast<const uint32_t*>(codes + kCodeBytes + meta_off);
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                if ((mw >> 16) != 0x7FFFu) {
-                    const uint32_t sp = __byte_perm(mw, mw, 0x1010), zp = __byte_perm(mw, mw, 0x3232);
+                const uint4 w0 = *reinterpret_cast<const uint4*>(codes + code0);
+                const uint4 w1 = *reinterpret_cast<const uint4*>(codes + code1);
+                const uint32_t mw[2] = {*reinterpret_cast<const uint32_t*>(codes + kCodeBytes + meta0),
+                                        *reinterpret_cast<const uint32_t*>(codes + kCodeBytes + meta1)};
+                const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t sp = __byte_perm(mw[c], mw[c], 0x1010), zp = __byte_perm(mw[c], mw[c], 0x3232);
                     const __half2 s2 = *reinterpret_cast<const __half2*>(&sp), z2 = *reinterpret_cast<const __half2*>(&zp);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 4 * c; j < 4 * c + 4; ++j) {
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -676,23 +725,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
                             const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&p), z2), s2);
                             o[e] = *reinterpret_cast<const uint32_t*>(&v);
                         }
-                        *reinterpret_cast<uint4*>(arow + 16 * ((chunk0 + j) ^ (row & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(arow + 16 * (j ^ (row & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                } else {
+                }
+                if ((mw[0] >> 16) == 0x7FFFu || (mw[1] >> 16) == 0x7FFFu) {  // rare: rewrite the far half row
                     const int64_t vrow = kBack ? (int64_t)ks * kBK + row : (int64_t)rt * kTileRows + rank * kBM + row;
                     const int64_t n = MODE == kGated ? gated_row(vrow, a.I) : vrow;
-                    const int g = kBack ? min((rt * kTileRows + rank * kBM + c * 32) / a.group, a.GQ - 1)
-                                        : (ks * kBK + c * 32) / a.group;
-                    const float sv = bf16_bits_to_float(__ldg(a.scales + n * a.GQ + g));
-                    const int z = __ldg(a.zeros + n * a.GQ + g), e2 = (int)(int16_t)(mw & 0xFFFFu);
+                    const int col = kBack ? rt * kTileRows + rank * kBM + h * 64 : ks * kBK;
 #pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t o[4];
-#pragma unroll 1
-                        for (int e = 0; e < 4; ++e)
-                            o[e] = far_value((w[j] >> (4 * e)) & 15u, sv, z, e2) |
-                                   (far_value((w[j] >> (4 * e + 16)) & 15u, sv, z, e2) << 16);
-                        *reinterpret_cast<uint4*>(arow + 16 * ((chunk0 + j) ^ (row & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int c = 0; c < 2; ++c) {
+                        if ((mw[c] >> 16) != 0x7FFFu) continue;
+                        const int g = min((col + 32 * c) / a.group, a.GQ - 1);
+                        far_half(arow, codes + (c ? code1 : code0), 4 * c, row & 7,
+                                 bf16_bits_to_float(__ldg(a.scales + n * a.GQ + g)), __ldg(a.zeros + n * a.GQ + g),
+                                 (int)(int16_t)(mw[c] & 0xFFFFu));
                     }
                 }
                 fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor core
