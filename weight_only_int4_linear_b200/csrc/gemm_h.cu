@@ -40,7 +40,8 @@
 // Warps: three groups of four dequantiser warps, which take the stages in turn (a
 // stage's dequantisation is a chain of waits -- copy, loads, stores, proxy fence --
 // longer than its MMAs), four epilogue warps (TMEM lane quadrants), TMA, MMA issue
-// (rank 0).  Two accumulators: a tile's epilogue overlaps the
+// (rank 0).  Tokens and codes are issued by two warps: with one thread issuing every
+// copy of a stage its instruction latency, about 800 cycles, bounded the kernel.  Two accumulators: a tile's epilogue overlaps the
 // next tile's MMAs.
 #include "decode_units.cuh"
 #include "epilogue.cuh"
@@ -57,12 +58,11 @@ constexpr int kBK = 64;                        // contraction per stage
 constexpr int kABytes = kBM * kBK * 2;         // 16 KB
 constexpr int kCodeBytes = kBM * kBK / 2;      // 4 KB
 constexpr int kMetaBytes = 1024;               // up to 8 lines of 128 B x ... (see meta words below)
-#ifndef W4A16_H_DQ_GROUPS
-#define W4A16_H_DQ_GROUPS 3
-#endif
-constexpr int kDqGroups = W4A16_H_DQ_GROUPS;   // groups of 4 dequantiser warps, each taking every kDqGroups-th stage
+constexpr int kDqGroups = 3;                   // groups of 4 dequantiser warps, each taking every kDqGroups-th stage
 constexpr int kDqWarps = 4 * kDqGroups, kEpiWarps = 4;
-constexpr int kTmaWarp = kDqWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kTokWarp = kDqWarps + kEpiWarps;  // TMA: tokens
+constexpr int kCodeWarp = kTokWarp + 1;         // TMA: codes and meta words
+constexpr int kMmaWarp = kCodeWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kTopExp = 15;                    // scaled operands stay below 2^15
 
@@ -73,7 +73,10 @@ struct Cfg {
     static constexpr int kXBytes = NT / 2 * kBK * 2;
     static constexpr int kStageBytes = kXBytes + kABytes + kCodeBytes + kMetaBytes;
     static constexpr int kFit = 226 * 1024 / kStageBytes;
-    static constexpr int kStages = kFit < 9 ? kFit : 9;
+    // A multiple of the dequantiser groups: a group then comes back to a stage on every round of the ring, and the
+    // parity it waits for cannot stand for an older round (copies complete in any order).
+    static constexpr int kStages = (kFit < 9 ? kFit : 9) / kDqGroups * kDqGroups;
+    static_assert(kStages % kDqGroups == 0 && kStages >= kDqGroups, "stages and dequantiser groups");
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;  // + alignment slack
     static constexpr uint32_t kTmemCols = 2 * NT;                          // two accumulators
     static_assert(kStageBytes % 1024 == 0 && kSmem + 512 <= 232448, "shared memory per CTA");
@@ -102,6 +105,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         "[%5];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // x 2^t for any t: two exact factors, so that only the result can leave the FP32 range.
@@ -557,7 +567,8 @@ __device__ __noinline__ void far_half(unsigned char* arow, const unsigned char* 
 
 template <int MODE, int NT>
 __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_constant__ CUtensorMap tx,
-                                                             const __grid_constant__ CUtensorMap tq, const HArgs a) {
+                                                             const __grid_constant__ CUtensorMap tq,
+                                                             const __grid_constant__ CUtensorMap tm, const HArgs a) {
     using C = Cfg<NT>;
     constexpr int S = C::kStages;
     constexpr bool kBack = MODE == kDx;
@@ -570,13 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
     unsigned char* ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // same offset in both CTAs
 
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const int rank = (int)cluster_ctarank();
     const int b = blockIdx.x / 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);       // the two TMA warps
             mbar_init(&afull[s], 4 * 2);  // one dequantiser group in each CTA
             mbar_init(&empty[s], 1);
         }
@@ -594,57 +605,66 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
     const uint32_t tmem = s_tmem;
     Segments seg(b, a);
 
-    if (warp == kTmaWarp) {  // ------------------------------------------------------------ TMA
-        if (lane == 0) {
-            prefetch_tmap(&tx);
-            prefetch_tmap(&tq);
-            pdl_wait_primary();  // operands and meta words come from the preparation kernels
-            Ring<S> r;
-            int issued = 0;
-            bool ok = true;
-            const int lg = a.group >> 6;  // log2(group / 32): 0, 1, 2
-            const int lines = kBack ? kBM / a.group : (lg == 0 ? 2 : 1);
-            const uint32_t line_bytes = (kBack ? kBK : kBM) * 4;
-            const uint32_t bytes = C::kXBytes + kCodeBytes + lines * line_bytes;
-            while (ok && seg.next(a)) {
-                int rt, mt;
-                tile_coords(seg.tile, a, rt, mt);
-                const int row0 = rt * kTileRows + rank * kBM;  // this CTA's first output row
-                const int tok0 = mt * NT + rank * (NT / 2);
-                // backward: groups of the CTA's columns; columns past K take any line (never stored)
-                const int gb = min(row0 >> (5 + lg), a.GQ - lines);
-                for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
-                    if (!mbar_wait(&empty[r.s], r.parity ^ 1u, a.fault, 171)) {
-                        ok = false;
-                        break;
-                    }
-                    uint64_t* bar = &full[r.s];
-                    unsigned char* st = ring + r.s * C::kStageBytes;
-                    unsigned char *codes = st + C::kXBytes + kABytes, *meta = codes + kCodeBytes;
-                    mbar_arrive_expect_tx(bar, bytes);
-                    tma_load_2d(st, &tx, ks * kBK, tok0, bar);
-                    if constexpr (kBack)  // 64 weight rows x 128 columns
-                        tma_load_2d(codes, &tq, row0 / 8, ks * kBK, bar);
-                    else if constexpr (MODE == kGated)
-                        tma_load_3d(codes, &tq, ks * (kBK / 8), 0, row0 / 2, bar);
-                    else
-                        tma_load_2d(codes, &tq, ks * (kBK / 8), row0, bar);
-                    // one line of meta words per group: forward 128 rows, backward 64
-                    const uint32_t* mp = kBack ? a.meta + (int64_t)gb * a.Rp + ks * kBK
-                                               : a.meta + (int64_t)(2 * ks >> lg) * a.Rp + row0;
-                    for (int l = 0; l < lines; ++l)
-                        bulk_load(meta + l * line_bytes, mp + (int64_t)l * a.Rp, line_bytes, bar);
-                    ++issued;
+    // The issuing warps run their loops with all lanes, so that positions and descriptors stay in uniform
+    // registers, and one elected lane issues: one thread's instruction latency per stage is what bounds them.
+    if (warp == kTokWarp || warp == kCodeWarp) {  // ------------------------------------------ TMA
+        const bool leader = elect_one();
+        const bool toks = warp == kTokWarp;
+        if (leader) {
+            prefetch_tmap(toks ? &tx : &tq);
+            if (!toks) prefetch_tmap(&tm);
+        }
+        pdl_wait_primary();  // operands and meta words come from the preparation kernels
+        Ring<S> r;
+        int issued = 0;
+        bool ok = true;
+        const int lg = a.group >> 6;  // log2(group / 32): 0, 1, 2
+        const int lines = kBack ? kBM / a.group : (lg == 0 ? 2 : 1);
+        const uint32_t bytes = toks ? C::kXBytes : kCodeBytes + lines * (kBack ? kBK : kBM) * 4;
+        while (ok && seg.next(a)) {
+            int rt, mt;
+            tile_coords(seg.tile, a, rt, mt);
+            const int row0 = rt * kTileRows + rank * kBM;  // this CTA's first output row
+            const int tok0 = mt * NT + rank * (NT / 2);
+            // backward: the first group of the CTA's columns (columns past K take any: they are never stored)
+            const int gb = min(row0 >> (5 + lg), a.GQ - lines);
+            for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
+                if (!mbar_wait(&empty[r.s], r.parity ^ 1u, a.fault, 171)) {
+                    ok = false;
+                    break;
                 }
-            }
-            // copies in flight land before the CTA may exit: the last S stages issued
-            for (int i = 0; i < min(issued, S); ++i) {
-                r.prev();
-                mbar_wait(&full[r.s], r.parity, a.fault, 172);
+                uint64_t* bar = &full[r.s];
+                unsigned char* st = ring + r.s * C::kStageBytes;
+                if (leader) {
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (toks) {
+                        tma_load_2d(st, &tx, ks * kBK, tok0, bar);
+                    } else {
+                        unsigned char* codes = st + C::kXBytes + kABytes;
+                        // codes, and one line of meta words per group: forward 128 rows, backward 64
+                        if constexpr (kBack) {
+                            tma_load_2d(codes, &tq, row0 / 8, ks * kBK, bar);
+                            tma_load_2d(codes + kCodeBytes, &tm, ks * kBK, gb, bar);
+                        } else {
+                            if constexpr (MODE == kGated)
+                                tma_load_3d(codes, &tq, ks * (kBK / 8), 0, row0 / 2, bar);
+                            else
+                                tma_load_2d(codes, &tq, ks * (kBK / 8), row0, bar);
+                            tma_load_2d(codes + kCodeBytes, &tm, row0, 2 * ks >> lg, bar);
+                        }
+                    }
+                }
+                ++issued;
             }
         }
+        // copies in flight land before the CTA may exit: the last S stages issued
+        for (int i = 0; i < min(issued, S); ++i) {
+            r.prev();
+            mbar_wait(&full[r.s], r.parity, a.fault, 172);
+        }
     } else if (warp == kMmaWarp) {  // ------------------------------------------------ MMA issue
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool leader = elect_one();
             Ring<S> r;
             int sc = 0;
             bool ok = true;
@@ -662,16 +682,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
                     }
                     tc_fence_after();
                     const uint64_t off = (uint64_t)(r.s * (C::kStageBytes >> 4));
+                    if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_ss_pair(tmem + buf * NT, adesc + off + kk * kAStep, xdesc + off + kk * kXStep, kIdesc,
-                                     ks > seg.s0 || kk > 0);
-                    umma_commit_pair(&empty[r.s], 0x3);
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            umma_ss_pair(tmem + buf * NT, adesc + off + kk * kAStep, xdesc + off + kk * kXStep, kIdesc,
+                                         ks > seg.s0 || kk > 0);
+                        umma_commit_pair(&empty[r.s], 0x3);
+                    }
                 }
-                if (ok) umma_commit_pair(&mdone[buf], 0x3);
+                if (ok && leader) umma_commit_pair(&mdone[buf], 0x3);
                 ++sc;
             }
-            umma_commit_pair(&drained, 0x1);  // every MMA issued completes before the teardown
+            if (leader) umma_commit_pair(&drained, 0x1);  // every MMA issued completes before the teardown
             mbar_wait(&drained, 0, a.fault, 175);
         }
     } else if (warp < kDqWarps) {  // ------------------------------------------------- dequantisers
@@ -889,7 +911,7 @@ int launch_pdl(Kern kernel, int64_t grid, int block, cudaStream_t stream, Args..
 }
 
 template <int MODE, int NT>
-int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, cudaStream_t stream) {
+int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, const CUtensorMap& tm, cudaStream_t stream) {
     using C = Cfg<NT>;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -942,16 +964,17 @@ int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, cudaStre
     const int busy = a.whole_tiles > 0 ? (a.whole_tiles < units ? a.whole_tiles : units) : 0;
     const int grid = busy > a.split_units ? busy : a.split_units;
     cfg.gridDim = dim3((unsigned)(grid * 2));
-    if (cudaLaunchKernelEx(&cfg, gemm_h_kernel<MODE, NT>, tx, tq, a) != cudaSuccess) return W4A16_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, gemm_h_kernel<MODE, NT>, tx, tq, tm, a) != cudaSuccess) return W4A16_ERR_CUDA;
     if (cut == 0) return W4A16_OK;
     return launch_pdl(gemm_h_join_kernel<MODE, NT>, (int64_t)cut * (NT / 8), kTileRows, stream, a);
 }
 
 template <int MODE>
-int launch_mode(int NT, const HArgs& a, const CUtensorMap& tx, const CUtensorMap& tq, cudaStream_t stream) {
-    return NT == 64    ? launch_tiles<MODE, 64>(a, tx, tq, stream)
-           : NT == 128 ? launch_tiles<MODE, 128>(a, tx, tq, stream)
-                       : launch_tiles<MODE, 256>(a, tx, tq, stream);
+int launch_mode(int NT, const HArgs& a, const CUtensorMap& tx, const CUtensorMap& tq, const CUtensorMap& tm,
+                cudaStream_t stream) {
+    return NT == 64    ? launch_tiles<MODE, 64>(a, tx, tq, tm, stream)
+           : NT == 128 ? launch_tiles<MODE, 128>(a, tx, tq, tm, stream)
+                       : launch_tiles<MODE, 256>(a, tx, tq, tm, stream);
 }
 
 }  // namespace
@@ -990,7 +1013,7 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     a.NS = (int)(K / kBK);
     a.m_tiles = (int)ceil_div(M, NT);
     a.r_tiles = (int)ceil_div(N, kTileRows);
-    CUtensorMap tx, tq;
+    CUtensorMap tx, tq, tm;
     if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + l.op, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kBK,
                         (uint32_t)NT / 2, CU_TENSOR_MAP_SWIZZLE_128B))
         return W4A16_ERR_CUDA;
@@ -999,7 +1022,10 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
                                              {kBK / 8, 2, kBM / 2}, CU_TENSOR_MAP_SWIZZLE_32B)
                             : encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N,
                                              (uint64_t)K / 2, kBK / 8, kBM, CU_TENSOR_MAP_SWIZZLE_32B);
-    if (!ok) return W4A16_ERR_CUDA;
+    // the meta words of a stage: 128 rows x the groups of its 64 k
+    if (!ok || !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
+                               (uint64_t)l.Rp * 4, kBM, group == 32 ? 2 : 1))
+        return W4A16_ERR_CUDA;
     const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int*>(ws + l.exps),
                       (int)N, (int)l.Rp, a.GQ, I};
     const TokenArgs t{X, xscale, reinterpret_cast<__half*>(ws + l.op), reinterpret_cast<int*>(ws + l.texp), (int)M,
@@ -1007,7 +1033,7 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     const int meta_blocks = (int)(l.Rp / kMetaRows);
     const int st = launch_pdl(prep_forward_kernel, meta_blocks + M, kPrepThreads, stream, ma, meta_blocks, t);
     if (st != W4A16_OK) return st;
-    return e.gated ? launch_mode<kGated>(NT, a, tx, tq, stream) : launch_mode<kLinear>(NT, a, tx, tq, stream);
+    return e.gated ? launch_mode<kGated>(NT, a, tx, tq, tm, stream) : launch_mode<kLinear>(NT, a, tx, tq, tm, stream);
 }
 
 int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU, int act, uint16_t* dGU, int64_t M,
@@ -1038,12 +1064,14 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     a.NS = (int)ceil_div(N, kBK);
     a.m_tiles = (int)ceil_div(M, NT);
     a.r_tiles = (int)ceil_div(K, kTileRows);
-    CUtensorMap tx, tq;
+    CUtensorMap tx, tq, tm;
     // rows of N values, Np apart: what lies past N is filled with zeros
     if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + l.op, (uint64_t)N, (uint64_t)M, (uint64_t)l.Cp * 2,
                         kBK, (uint32_t)NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N, (uint64_t)K / 2,
-                        kBM / 8, kBK, CU_TENSOR_MAP_SWIZZLE_64B))
+                        kBM / 8, kBK, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
+                        (uint64_t)l.Rp * 4, kBK, (uint32_t)(kBM / group)))  // 64 rows x the groups of 128 columns
         return W4A16_ERR_CUDA;
     const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int*>(ws + l.exps),
                       (int)N, (int)l.Rp, a.GQ, 0};
@@ -1069,7 +1097,7 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
         st = N % 8 == 0 ? launch_pdl(prep_grad_kernel<8, false>, M, kGradThreads, stream, g)
                         : launch_pdl(prep_grad_kernel<1, false>, M, kGradThreads, stream, g);
     if (st != W4A16_OK) return st;
-    return launch_mode<kDx>(NT, a, tx, tq, stream);
+    return launch_mode<kDx>(NT, a, tx, tq, tm, stream);
 }
 
 }  // namespace w4a16
