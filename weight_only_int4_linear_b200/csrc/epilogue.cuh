@@ -28,50 +28,86 @@ constexpr float kGeluA = 0.044715f;
 constexpr float kRsqrt2 = 0.7071067811865476f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;
 
-// act(x).  GELU by erfc and by a sigmoid (0.5 (1 + tanh u) = sigmoid(2 u)): neither form cancels for negative x.
-__device__ __forceinline__ float act_f(float x, int act) {
-    switch (act) {
-        case W4A16_ACT_RELU: return x < 0.f ? 0.f : x;  // NaN stays NaN
-        case W4A16_ACT_SILU: return x < -88.f ? x * __expf(x) : x * sigmoid_f(x);
-        case W4A16_ACT_GELU: return 0.5f * x * erfcf(-x * kRsqrt2);
-        case W4A16_ACT_GELU_TANH: {
-            const float u = 2.f * kGeluC * (x + kGeluA * x * x * x);
-            return u < -88.f ? x * __expf(u) : x * sigmoid_f(u);
-        }
-        default: return x;
-    }
+__device__ __forceinline__ float silu_f(float x) { return x < -88.f ? x * __expf(x) : x * sigmoid_f(x); }
+// GELU by erfc and by a sigmoid (0.5 (1 + tanh u) = sigmoid(2 u)): neither form cancels for negative x.
+__device__ __forceinline__ float gelu_f(float x) { return 0.5f * x * erfcf(-x * kRsqrt2); }
+__device__ __forceinline__ float gelu_tanh_f(float x) {
+    const float u = 2.f * kGeluC * (x + kGeluA * x * x * x);
+    return u < -88.f ? x * __expf(u) : x * sigmoid_f(u);
 }
 
-// act(x) and act'(x).
-__device__ __forceinline__ void act_grad_f(float x, int act, float& f, float& d) {
+// x[j] = act(x[j]); the choice is uniform over the grid.
+template <int T>
+__device__ __forceinline__ void act_all(float (&x)[T], int act) {
     switch (act) {
         case W4A16_ACT_RELU:
-            f = x < 0.f ? 0.f : x;
-            d = x > 0.f ? 1.f : 0.f;  // 0 at 0
-            return;
-        case W4A16_ACT_SILU: {
-            const float s = x < -88.f ? __expf(x) : sigmoid_f(x), t = sigmoid_f(-x);
-            f = x * s;
-            d = s * (1.f + x * t);
-            return;
-        }
-        case W4A16_ACT_GELU: {
-            const float p = 0.5f * erfcf(-x * kRsqrt2);
-            f = x * p;
-            d = p + x * kRsqrt2Pi * __expf(-0.5f * x * x);
-            return;
-        }
-        case W4A16_ACT_GELU_TANH: {
-            const float x2 = x * x, u = 2.f * kGeluC * (x + kGeluA * x2 * x);
-            const float s = u < -88.f ? __expf(u) : sigmoid_f(u), t = sigmoid_f(-u);
-            f = x * s;
-            // s t vanishes long before the cubic factor overflows; past |x| = 30 it is zero in FP32
-            d = fabsf(x) > 30.f ? s : s + x * s * t * 2.f * kGeluC * (1.f + 3.f * kGeluA * x2);
-            return;
-        }
+#pragma unroll
+            for (int j = 0; j < T; ++j) x[j] = x[j] < 0.f ? 0.f : x[j];  // NaN stays NaN
+            break;
+        case W4A16_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < T; ++j) x[j] = silu_f(x[j]);
+            break;
+        case W4A16_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < T; ++j) x[j] = gelu_f(x[j]);
+            break;
+        case W4A16_ACT_GELU_TANH:
+#pragma unroll
+            for (int j = 0; j < T; ++j) x[j] = gelu_tanh_f(x[j]);
+            break;
+        default: break;
+    }
+}
+__device__ __forceinline__ float act_f(float x, int act) {
+    float v[1] = {x};
+    act_all<1>(v, act);
+    return v[0];
+}
+
+// f[j] = act(x[j]), d[j] = act'(x[j]).  1 - s loses bits only where it is a small part of act'.
+template <int T>
+__device__ __forceinline__ void act_grads(const float (&x)[T], int act, float (&f)[T], float (&d)[T]) {
+    switch (act) {
+        case W4A16_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                f[j] = x[j] < 0.f ? 0.f : x[j];
+                d[j] = x[j] > 0.f ? 1.f : 0.f;  // 0 at 0
+            }
+            break;
+        case W4A16_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                const float s = x[j] < -88.f ? __expf(x[j]) : sigmoid_f(x[j]);
+                f[j] = x[j] * s;
+                d[j] = s + f[j] * (1.f - s);
+            }
+            break;
+        case W4A16_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                const float p = 0.5f * erfcf(-x[j] * kRsqrt2);
+                f[j] = x[j] * p;
+                d[j] = p + x[j] * kRsqrt2Pi * __expf(-0.5f * x[j] * x[j]);
+            }
+            break;
+        case W4A16_ACT_GELU_TANH:
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                const float x2 = x[j] * x[j], u = 2.f * kGeluC * (x[j] + kGeluA * x2 * x[j]);
+                const float s = u < -88.f ? __expf(u) : sigmoid_f(u);
+                f[j] = x[j] * s;
+                // s (1 - s) vanishes long before the cubic factor overflows: past |x| = 30 it is zero in FP32
+                d[j] = fabsf(x[j]) > 30.f ? s : s + f[j] * (1.f - s) * 2.f * kGeluC * (1.f + 3.f * kGeluA * x2);
+            }
+            break;
         default:
-            f = x;
-            d = 1.f;
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                f[j] = x[j];
+                d[j] = 1.f;
+            }
     }
 }
 

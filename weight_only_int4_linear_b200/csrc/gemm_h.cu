@@ -39,7 +39,7 @@
 //
 // Warps: three groups of four dequantiser warps, which take the stages in turn (a
 // stage's dequantisation is a chain of waits -- copy, loads, stores, proxy fence --
-// longer than its MMAs), four epilogue warps (TMEM lane quadrants), TMA, MMA issue
+// longer than its MMAs), eight epilogue warps (two per TMEM lane quadrant), TMA, MMA issue
 // (rank 0).  Tokens and codes are issued by two warps: with one thread issuing every
 // copy of a stage its instruction latency, about 800 cycles, bounded the kernel.  Two accumulators: a tile's epilogue overlaps the
 // next tile's MMAs.
@@ -47,6 +47,7 @@
 #include "epilogue.cuh"
 #include "sm100.cuh"
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 namespace w4a16 {
@@ -59,7 +60,7 @@ constexpr int kABytes = kBM * kBK * 2;         // 16 KB
 constexpr int kCodeBytes = kBM * kBK / 2;      // 4 KB
 constexpr int kMetaBytes = 1024;               // up to 8 lines of 128 B x ... (see meta words below)
 constexpr int kDqGroups = 3;                   // groups of 4 dequantiser warps, each taking every kDqGroups-th stage
-constexpr int kDqWarps = 4 * kDqGroups, kEpiWarps = 4;
+constexpr int kDqWarps = 4 * kDqGroups, kEpiWarps = 8;  // two epilogue warps per TMEM lane quadrant
 constexpr int kTokWarp = kDqWarps + kEpiWarps;  // TMA: tokens
 constexpr int kCodeWarp = kTokWarp + 1;         // TMA: codes and meta words
 constexpr int kMmaWarp = kCodeWarp + 1;
@@ -114,12 +115,16 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// x 2^t for any t: two exact factors, so that only the result can leave the FP32 range.
+// x 2^t: two exact factors, so that only the result can leave the FP32 range.  Past +-252 the callers' results are
+// zero or infinite either way.
 __device__ __forceinline__ float scale2(float x, int t) {
-    t = min(max(t, -280), 252);
+    t = min(max(t, -252), 252);
     const int h = t >> 1;
-    return x * pow2f(h) * pow2f(t - h);
+    return x * __uint_as_float((uint32_t)(h + 127) << 23) * __uint_as_float((uint32_t)(t - h + 127) << 23);
 }
+
+// FP32 -> BF16 bits, nearest even, as one conversion instruction.
+__device__ __forceinline__ uint16_t to_bf16(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
 // Output row v of a gated weight's interleaved order -> weight row.
 __device__ __forceinline__ int64_t gated_row(int64_t v, int64_t I) { return (v & 1) * I + (v >> 1); }
@@ -131,69 +136,76 @@ __device__ __forceinline__ int64_t gated_row(int64_t v, int64_t I) { return (v &
 // half: the dequantiser then forms the value in binary64 from the stored scale and zero point.  Rows past the
 // matrix get zero words (s' = 0).  exps[v] = e of row v.
 constexpr int kPrepThreads = 256;
-constexpr int kMetaRows = 32;  // rows per block
+constexpr int kMetaRows = kPrepThreads / 32;  // rows per block: a warp each (8 words of a line: one 32-byte sector)
+constexpr int kMetaChunk = 128;               // groups per step: four loads in flight per lane
 
 struct MetaArgs {
     const uint16_t* scales;
     const int32_t* zeros;
     uint32_t* meta;
-    int* exps;
+    int16_t* exps;  // [Rp] e
+    float* pows;    // [Rp] 2^e (backward), 0 where it is no normal FP32 number
     int R, Rp, GQ;
-    int64_t I;  // gated: rows per half, else 0
+    int64_t I;      // gated: rows per half, else 0
 };
 
-__device__ __forceinline__ int bf16_exponent(uint32_t bits) {  // floor(log2 |x|), or below it for subnormals
+__device__ __forceinline__ int bf16_exponent(uint32_t bits) {  // floor(log2 |x|), or above it for subnormals
     const int ef = (int)((bits >> 7) & 0xFF);
     return ef == 0 ? -126 : ef - 127;
 }
+constexpr int kNothing = -100000;  // exponent of zero
 
 __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
-    __shared__ uint32_t s_word[kMetaRows][33];
-    __shared__ int s_exp[kMetaRows];
+    __shared__ uint32_t s_word[kMetaRows][kMetaChunk + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int v0 = block * kMetaRows;
-    constexpr int RPW = kMetaRows / (kPrepThreads / 32);  // rows per warp
-    for (int i = 0; i < RPW; ++i) {
-        const int v = v0 + warp * RPW + i;
-        int top = -100000;
-        if (v < a.R) {
-            const int64_t n = a.I ? gated_row(v, a.I) : v;
-            for (int g = lane; g < a.GQ; g += 32) {
-                const uint32_t sb = __ldg(a.scales + n * a.GQ + g);
-                const long long z = __ldg(a.zeros + n * a.GQ + g);
-                const long long mag = max(z < 0 ? -z : z, 15 - z < 0 ? z - 15 : 15 - z);
-                // |(q - z) s| < 2^(exponent + 1 + bits of mag)
-                if (sb & 0x7FFFu) top = max(top, bf16_exponent(sb) + 1 + (64 - __clzll(mag)));
-            }
+    const int v0 = block * kMetaRows, v = v0 + warp;
+    const bool row_ok = v < a.R;
+    const int64_t n = row_ok ? (a.I ? gated_row(v, a.I) : v) : 0;
+    const uint16_t* sc = a.scales + n * a.GQ;
+    const int32_t* ze = a.zeros + n * a.GQ;
+    constexpr int L = kMetaChunk / 32;
+    int top = kNothing;
+    for (int g0 = 0; g0 < a.GQ; g0 += kMetaChunk) {
+        uint32_t sb[L];
+        int z[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int g = g0 + 32 * i + lane;
+            const bool ok = row_ok && g < a.GQ;
+            sb[i] = ok ? __ldg(sc + g) : 0u;
+            z[i] = ok ? __ldg(ze + g) : 0;
         }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (lane == 0) {
-            const int e = top == -100000 ? 0 : top - kTopExp;
-            s_exp[warp * RPW + i] = e;
-            if (v < a.Rp) a.exps[v] = e;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            // |q - z| <= max(|z|, |15 - z|) < 2^bits, |s| < 2^(exponent + 1)
+            const uint32_t mag = z[i] < 8 ? 15u - (uint32_t)z[i] : (uint32_t)z[i];
+            if (sb[i] & 0x7FFFu) top = max(top, bf16_exponent(sb[i]) + 1 + (32 - __clz(mag)));
         }
     }
-    __syncthreads();
-    for (int g0 = 0; g0 < a.GQ; g0 += 32) {
-        for (int i = 0; i < RPW; ++i) {
-            const int r = warp * RPW + i, v = v0 + r, g = g0 + lane;
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const int e = top == kNothing ? 0 : top - kTopExp;
+    if (lane == 0) {
+        a.exps[v] = (int16_t)e;
+        if (a.pows) a.pows[v] = e >= -126 && e <= 127 ? __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
+    }
+    for (int g0 = 0; g0 < a.GQ; g0 += kMetaChunk) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int g = g0 + 32 * i + lane;
             uint32_t word = 0;
-            if (v < a.R && g < a.GQ) {
-                const int64_t n = a.I ? gated_row(v, a.I) : v;
-                const int z = __ldg(a.zeros + n * a.GQ + g), e = s_exp[r];
-                if (z >= -1024 && z <= 1024) {
-                    const float s = scale2(bf16_bits_to_float(__ldg(a.scales + n * a.GQ + g)), -e);
-                    word = (uint32_t)__half_as_ushort(__float2half_rn(s)) |
-                           ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16);
-                } else {
-                    word = ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
-                }
+            if (row_ok && g < a.GQ) {
+                const int z = __ldg(ze + g);
+                const float s = scale2(bf16_bits_to_float(__ldg(sc + g)), -e);
+                word = z >= -1024 && z <= 1024 ? (uint32_t)__half_as_ushort(__float2half_rn(s)) |
+                                                     ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16)
+                                               : ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
             }
-            s_word[r][lane] = word;
+            s_word[warp][32 * i + lane] = word;
         }
         __syncthreads();
-        for (int g = warp; g < 32 && g0 + g < a.GQ; g += kPrepThreads / 32)
-            if (v0 + lane < a.Rp) a.meta[(int64_t)(g0 + g) * a.Rp + v0 + lane] = s_word[lane][g];
+        const int r = threadIdx.x % kMetaRows;
+        for (int g = threadIdx.x / kMetaRows; g < min(kMetaChunk, a.GQ - g0); g += kPrepThreads / kMetaRows)
+            a.meta[(int64_t)(g0 + g) * a.Rp + v0 + r] = s_word[r][g];
         __syncthreads();
     }
 }
@@ -206,12 +218,12 @@ __device__ __forceinline__ int block_max(int v) {
     __syncthreads();
     if (lane == 0) s_max[warp] = v;
     __syncthreads();
-    v = lane < (int)(blockDim.x >> 5) ? s_max[lane] : -100000;
+    v = lane < (int)(blockDim.x >> 5) ? s_max[lane] : kNothing;
     return __reduce_max_sync(0xFFFFFFFFu, v);
 }
 
 // Row exponent a from the largest exponent E (|x| < 2^(E + 1)): x 2^-a < 2^15.
-__device__ __forceinline__ int row_exp(int E) { return E == -100000 ? 0 : E + 1 - kTopExp; }
+__device__ __forceinline__ int row_exp(int E) { return E == kNothing ? 0 : E + 1 - kTopExp; }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -256,7 +268,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_forward_kernel(const MetaAr
 #pragma unroll
         for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
     }
-    const int a = row_exp(block_max(top ? bf16_exponent(top) : -100000));
+    const int a = row_exp(block_max(top ? bf16_exponent(top) : kNothing));
     const int h = -a >> 1;
     const float f1 = pow2f(h), f2 = pow2f(-a - h);  // |a| <= 150: both factors are FP32 powers of two
     if (threadIdx.x == 0) t.texp[m] = a;
@@ -281,16 +293,22 @@ __global__ void __launch_bounds__(kPrepThreads) prep_meta_kernel(const MetaArgs 
 }
 
 // Backward preparation, one block per token: the FP16 operand D'[m][n] = dY[m][n] 2^(e_n - a_m), row stride Np.
-// dY is read, or (dH given) formed as [dG | dU] from dH and GU = [G | U] and also stored as BF16:
+// dY is read, or (GATED) formed as [dG | dU] from dH and GU = [G | U] and also stored as BF16:
 //   dG = dH U act'(G),  dU = dH act(G).
-// Two passes over the row (the second from L2): the row's exponent first, then the values; dGU may be GU itself,
-// since a thread reads its elements of GU in the second pass before it writes them.  V: elements per load, 8 or 1.
+// The first pass over the row (from memory) finds an upper bound of its largest |dY 2^e| -- exact without GATED,
+// |dH| max(2 |U|, |G|) with it, which needs no activation (|act'| <= 1.13, |act(G)| <= |G|) -- and the second (from
+// L2) forms and stores the values.  Where a gated row turns out 2^-16 or more below its bound (every gate shut), its
+// operand is stored again with its true exponent, from the BF16 gradients just stored: dGU may be GU itself (a thread
+// reads its elements of GU before it writes them), which is then gone.
+// The scaling is a product by 2^e and one by 2^-a in FP32 where both and the row's bound are far from the ends of
+// its range, else in integer exponents.
 struct GradArgs {
     const uint16_t* dY;
     const uint16_t* dH;
     const uint16_t* GU;
     uint16_t* dGU;
-    const int* exps;  // [>= N] e_n
+    const int16_t* exps;  // [>= N] e_n
+    const float* pows;    // [>= N] 2^e_n, or 0
     __half* Dh;
     int* texp;
     int N, I, act;
@@ -298,123 +316,247 @@ struct GradArgs {
 };
 constexpr int kGradThreads = 512;
 
-template <int V>
-__device__ __forceinline__ void load_bf(const uint16_t* p, float (&f)[V]) {
-    if constexpr (V == 8) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __uint_as_float(w[j] << 16);
-            f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-    } else {
-        f[0] = bf16_bits_to_float(*p);
+// Eight elements of a row per thread and step: consecutive ones (VEC: rows 16-byte aligned), or 512 apart.
+template <bool VEC>
+struct Lane8 {
+    __device__ __forceinline__ static int first(int step) {
+        return VEC ? (step * kGradThreads + (int)threadIdx.x) * 8 : step * kGradThreads * 8 + (int)threadIdx.x;
     }
-}
-template <int V>
-__device__ __forceinline__ void store_bf(uint16_t* p, const float (&f)[V]) {
-    if constexpr (V == 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = (uint32_t)float_to_bf16_bits(f[2 * j]) | ((uint32_t)float_to_bf16_bits(f[2 * j + 1]) << 16);
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        *p = float_to_bf16_bits(f[0]);
-    }
-}
-template <int V>
-__device__ __forceinline__ void load_exps(const int* p, int (&e)[V]) {
-    if constexpr (V == 8) {
-        const int4 a = __ldcg(reinterpret_cast<const int4*>(p)), b = __ldcg(reinterpret_cast<const int4*>(p + 4));
-        e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w;
-        e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
-    } else {
-        e[0] = __ldcg(p);
-    }
-}
-// exponent of an FP32 value plus e; zero counts as nothing
-__device__ __forceinline__ int exp_of(float x, int e) {
-    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-    return u == 0 ? -100000 : max((int)(u >> 23), 1) - 127 + e;
-}
-template <int V>
-__device__ __forceinline__ void store_half(__half* p, const float (&f)[V], const int (&e)[V], int a) {
-    if constexpr (V == 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = half2_bits(scale2(f[2 * j], e[2 * j] - a), scale2(f[2 * j + 1], e[2 * j + 1] - a));
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        *p = __float2half_rn(scale2(f[0], e[0] - a));
-    }
-}
+    __device__ __forceinline__ static int at(int i, int j) { return VEC ? i + j : i + j * kGradThreads; }
 
-template <int V, bool GATED>
-__global__ void __launch_bounds__(kGradThreads) prep_grad_kernel(const GradArgs g) {
+    __device__ __forceinline__ static void load(const uint16_t* p, int i, int n, float (&f)[8]) {
+        if constexpr (VEC) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[2 * j] = __uint_as_float(w[j] << 16);
+                f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = at(i, j) < n ? bf16_bits_to_float(p[at(i, j)]) : 0.f;
+        }
+    }
+    __device__ __forceinline__ static void load(const float* p, int i, int n, bool vec, float (&f)[8]) {
+        if (VEC && vec) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(p + i)), b = __ldcg(reinterpret_cast<const float4*>(p + i + 4));
+            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = at(i, j) < n ? __ldcg(p + at(i, j)) : 1.f;
+        }
+    }
+    __device__ __forceinline__ static void load(const int16_t* p, int i, int n, int (&e)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = at(i, j) < n ? (int)__ldcg(p + at(i, j)) : 0;
+    }
+    __device__ __forceinline__ static void store_bf(uint16_t* p, int i, int n, const float (&f)[8]) {
+        if constexpr (VEC) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (at(i, j) < n) p[at(i, j)] = to_bf16(f[j]);
+        }
+    }
+    __device__ __forceinline__ static void store_half(__half* p, int i, int n, const float (&f)[8]) {
+        if constexpr (VEC) {
+            *reinterpret_cast<uint4*>(p + i) = make_uint4(half2_bits(f[0], f[1]), half2_bits(f[2], f[3]),
+                                                          half2_bits(f[4], f[5]), half2_bits(f[6], f[7]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (at(i, j) < n) p[at(i, j)] = __float2half_rn(f[j]);
+        }
+    }
+};
+
+// floor(log2 |x|) of an FP32 value, or above it for subnormals; zero counts as nothing
+__device__ __forceinline__ int exp_of(float x) {
+    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+    return u == 0 ? kNothing : max((int)(u >> 23), 1) - 127;
+}
+// Bits a gated row may stay under its bound before it is stored again: FP16 has 29 binades of full precision, so that
+// 16 leave the row's largest 13, and steps of 2^-24 of its largest value below them.
+constexpr int kFarBelow = 16;
+
+template <bool VEC, bool GATED>
+__global__ void __launch_bounds__(kGradThreads, 2) prep_grad_kernel(const GradArgs g) {
+    using L = Lane8<VEC>;
     pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t m = blockIdx.x;
+    const int n = GATED ? g.I : g.N;  // elements per sweep
+    const int steps = (n + kGradThreads * 8 - 1) / (kGradThreads * 8);
     __half* out = g.Dh + m * g.Np;
-    int top = -100000;
-    if constexpr (GATED) {
-        const uint16_t *dh = g.dH + m * g.I, *gu = g.GU + m * g.N;
-        uint16_t* dgu = g.dGU + m * g.N;
-        auto grads = [&](int i, float (&dg)[V], float (&du)[V]) {
-            float d[V], gg[V], uu[V];
-            load_bf<V>(dh + i, d);
-            load_bf<V>(gu + i, gg);
-            load_bf<V>(gu + g.I + i, uu);
+    const uint16_t* d0 = GATED ? g.dH + m * g.I : g.dY + m * g.N;
+    const uint16_t* gu = GATED ? g.GU + m * g.N : nullptr;
+    uint16_t* dgu = GATED ? g.dGU + m * g.N : nullptr;
+
+    float bound = 0.f, least = 1.f;
+#pragma unroll 2
+    for (int s = 0; s < steps; ++s) {
+        const int i = L::first(s);
+        if (i >= n) break;
+        float d[8], p[8];
+        L::load(d0, i, n, d);
+        L::load(g.pows, i, n, true, p);
+        if constexpr (GATED) {
+            float gg[8], uu[8], q[8];
+            L::load(gu, i, n, gg);
+            L::load(gu + g.I, i, n, uu);
+            L::load(g.pows + g.I, i, n, true, q);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float f, df;
-                act_grad_f(gg[j], g.act, f, df);
-                dg[j] = d[j] * uu[j] * df;
-                du[j] = d[j] * f;
+            for (int j = 0; j < 8; ++j) {
+                bound = fmaxf(bound, fmaxf(fabsf(2.f * d[j] * uu[j]) * p[j], fabsf(d[j] * gg[j]) * q[j]));
+                least = fminf(least, fminf(p[j], q[j]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                bound = fmaxf(bound, fabsf(d[j]) * p[j]);
+                least = fminf(least, p[j]);
+            }
+        }
+    }
+    // fast: every 2^e a normal number, and the bound so far inside FP32's range that neither 2^e nor the values
+    // that matter (down to 2^-40 of it) can leave it
+    const int E = block_max(exp_of(bound));
+    const bool odd = !(least > 0.f) || E >= 100;
+    const bool fast = !__syncthreads_or(odd) && E >= -70;
+
+    // values of step s: dG, dU (or dY in v)
+    auto values = [&](int i, float (&v)[8], float (&u)[8]) {
+        float d[8];
+        L::load(d0, i, n, d);
+        if constexpr (GATED) {
+            float gg[8], uu[8];
+            L::load(gu, i, n, gg);
+            L::load(gu + g.I, i, n, uu);
+            act_grads<8>(gg, g.act, u, v);  // u = act, v = act'
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] *= d[j] * uu[j];
+                u[j] *= d[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = d[j];
+        }
+    };
+
+    if (fast) {
+        int a = row_exp(E);
+        float fa = __uint_as_float((uint32_t)(127 - a) << 23);  // |a| <= 115
+        float most = 0.f;  // largest scaled value
+        for (int s = 0; s < steps; ++s) {
+            const int i = L::first(s);
+            if (i >= n) break;
+            float v[8], u[8], p[8];
+            values(i, v, u);
+            if constexpr (GATED) L::store_bf(dgu, i, n, v);
+            L::load(g.pows, i, n, true, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = v[j] * p[j] * fa;
+                most = fmaxf(most, fabsf(v[j]));
+            }
+            L::store_half(out, i, n, v);
+            if constexpr (GATED) {
+                L::store_bf(dgu + g.I, i, n, u);
+                L::load(g.pows + g.I, i, n, true, p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    u[j] = u[j] * p[j] * fa;
+                    most = fmaxf(most, fabsf(u[j]));
+                }
+                L::store_half(out + g.I, i, n, u);
+            }
+        }
+        if constexpr (!GATED) {
+            if (threadIdx.x == 0) g.texp[m] = a;
+            return;
+        }
+        const int top = block_max(exp_of(most));  // 14 where the bound was tight
+        if (top == kNothing || top >= kTopExp - 1 - kFarBelow) {
+            if (threadIdx.x == 0) g.texp[m] = a;
+            return;
+        }
+    }
+    if constexpr (GATED) {
+        // rows far below their bound, and rows at the ends of the range.  GU may have been overwritten by dGU
+        // (fast rows): those start from the BF16 gradients.
+        int top = kNothing;
+        auto each = [&](auto&& use) {
+            for (int s = 0; s < steps; ++s) {
+                const int i = L::first(s);
+                if (i >= n) break;
+                float v[8], u[8];
+                if (fast) {
+                    L::load(dgu, i, n, v);
+                    L::load(dgu + g.I, i, n, u);
+                } else {
+                    values(i, v, u);
+                }
+                int ev[8], eu[8];
+                L::load(g.exps, i, n, ev);
+                L::load(g.exps + g.I, i, n, eu);
+                use(i, v, u, ev, eu);
             }
         };
-        for (int i = threadIdx.x * V; i < g.I; i += kGradThreads * V) {
-            float dg[V], du[V];
-            int eg[V], eu[V];
-            grads(i, dg, du);
-            load_exps<V>(g.exps + i, eg);
-            load_exps<V>(g.exps + g.I + i, eu);
+        each([&](int i, float (&v)[8], float (&u)[8], int (&ev)[8], int (&eu)[8]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) top = max(top, max(exp_of(dg[j], eg[j]), exp_of(du[j], eu[j])));
-        }
-        const int a = row_exp(block_max(top));
+            for (int j = 0; j < 8; ++j) top = max(top, max(exp_of(v[j]) + ev[j], exp_of(u[j]) + eu[j]));
+        });
+        top = block_max(top < kNothing / 2 ? kNothing : top);
+        const int a = row_exp(top);
         if (threadIdx.x == 0) g.texp[m] = a;
-        for (int i = threadIdx.x * V; i < g.I; i += kGradThreads * V) {
-            float dg[V], du[V];
-            int eg[V], eu[V];
-            grads(i, dg, du);
-            load_exps<V>(g.exps + i, eg);
-            load_exps<V>(g.exps + g.I + i, eu);
-            store_bf<V>(dgu + i, dg);
-            store_bf<V>(dgu + g.I + i, du);
-            store_half<V>(out + i, dg, eg, a);
-            store_half<V>(out + g.I + i, du, eu, a);
-        }
+        each([&](int i, float (&v)[8], float (&u)[8], int (&ev)[8], int (&eu)[8]) {
+            if (!fast) {
+                L::store_bf(dgu, i, n, v);
+                L::store_bf(dgu + g.I, i, n, u);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = scale2(v[j], ev[j] - a);
+                u[j] = scale2(u[j], eu[j] - a);
+            }
+            L::store_half(out, i, n, v);
+            L::store_half(out + g.I, i, n, u);
+        });
     } else {
-        const uint16_t* dy = g.dY + m * g.N;
-        for (int i = threadIdx.x * V; i < g.N; i += kGradThreads * V) {
-            float d[V];
-            int e[V];
-            load_bf<V>(dy + i, d);
-            load_exps<V>(g.exps + i, e);
+        int top = kNothing;
+        for (int s = 0; s < steps; ++s) {
+            const int i = L::first(s);
+            if (i >= n) break;
+            float d[8];
+            int e[8];
+            L::load(d0, i, n, d);
+            L::load(g.exps, i, n, e);
 #pragma unroll
-            for (int j = 0; j < V; ++j) top = max(top, exp_of(d[j], e[j]));
+            for (int j = 0; j < 8; ++j) top = max(top, exp_of(d[j]) + e[j]);
         }
-        const int a = row_exp(block_max(top));
+        top = block_max(top < kNothing / 2 ? kNothing : top);
+        const int a = row_exp(top);
         if (threadIdx.x == 0) g.texp[m] = a;
-        for (int i = threadIdx.x * V; i < g.N; i += kGradThreads * V) {
-            float d[V];
-            int e[V];
-            load_bf<V>(dy + i, d);
-            load_exps<V>(g.exps + i, e);
-            store_half<V>(out + i, d, e, a);
+        for (int s = 0; s < steps; ++s) {
+            const int i = L::first(s);
+            if (i >= n) break;
+            float d[8];
+            int e[8];
+            L::load(d0, i, n, d);
+            L::load(g.exps, i, n, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = scale2(d[j], e[j] - a);
+            L::store_half(out, i, n, d);
         }
     }
 }
@@ -423,7 +565,7 @@ __global__ void __launch_bounds__(kGradThreads) prep_grad_kernel(const GradArgs 
 
 struct HArgs {
     const uint32_t* meta;
-    const int* exps;      // forward: e of every output row
+    const int16_t* exps;  // forward: e of every output row
     const int* texp;      // a of every token
     const uint16_t* scales;
     const int32_t* zeros;
@@ -502,51 +644,76 @@ struct Ring {
 // starts inside a tile (its first) and one that starts a tile and does not end it (its last).
 __device__ __forceinline__ int slot_of(int b, int s0) { return 2 * b + (s0 == 0 ? 1 : 0); }
 
-// Finishes T tokens of one output row: sum[j] belongs to token m0 + j and output row v.  All lanes of a warp call
-// it together, with consecutive v from an even one (gated rows are exchanged between neighbours).
+// What T tokens of an output row need beside their sums, loaded ahead of them: the tokens' exponents (m0 a multiple
+// of 4; texp has room for whole tiles) and the residual.
 template <int MODE, int T>
-__device__ __forceinline__ void finish(const HArgs& a, float (&sum)[T], int m0, int v, float bias, int row_e,
-                                       float col_s) {
-    const bool row_ok = v < a.R;
-    float y[T];
+struct Extra {
+    int te[T];
+    uint16_t res[MODE == kLinear ? T : 1];
+    __device__ __forceinline__ void load(const HArgs& a, int m0, int v) {
 #pragma unroll
-    for (int j = 0; j < T; j += 4) {  // m0 a multiple of 4; texp has room for whole tiles
-        const int4 t = __ldcg(reinterpret_cast<const int4*>(a.texp + m0 + j));
-        y[j] = scale2(sum[j], row_e + t.x);
-        y[j + 1] = scale2(sum[j + 1], row_e + t.y);
-        y[j + 2] = scale2(sum[j + 2], row_e + t.z);
-        y[j + 3] = scale2(sum[j + 3], row_e + t.w);
+        for (int j = 0; j < T; j += 4) {
+            const int4 t = __ldcg(reinterpret_cast<const int4*>(a.texp + m0 + j));
+            te[j] = t.x;
+            te[j + 1] = t.y;
+            te[j + 2] = t.z;
+            te[j + 3] = t.w;
+        }
+        if constexpr (MODE == kLinear) {
+            const uint16_t* r = a.ep.residual + (int64_t)m0 * a.R + v;
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+                res[j] = a.ep.residual && v < a.R && m0 + j < a.M ? __ldcg(r + (int64_t)j * a.R) : (uint16_t)0;
+        }
     }
-    if constexpr (MODE == kDx) {
+};
+
+// Finishes T tokens of one output row: y[j] (the raw sum) belongs to token m0 + j and output row v.  All lanes of a
+// warp call it together, with consecutive v from an even one (gated rows are exchanged between neighbours).
+template <int MODE, int T>
+__device__ __forceinline__ void finish(const HArgs& a, float (&y)[T], const Extra<MODE, T>& x, int m0, int v,
+                                       float bias, int row_e, float col_s) {
+    const bool row_ok = v < a.R;
+#pragma unroll
+    for (int j = 0; j < T; ++j) y[j] = scale2(y[j], row_e + x.te[j]);
+    if constexpr (MODE != kGated) {
+        if constexpr (MODE == kDx) {
+#pragma unroll
+            for (int j = 0; j < T; ++j) y[j] *= col_s;
+        } else {
+#pragma unroll
+            for (int j = 0; j < T; ++j) y[j] += bias;
+            act_all<T>(y, a.ep.act);
+#pragma unroll
+            for (int j = 0; j < T; ++j) y[j] += bf16_bits_to_float(x.res[j]);
+        }
+        uint16_t* out = a.Y + (int64_t)m0 * a.R + v;
 #pragma unroll
         for (int j = 0; j < T; ++j)
-            if (row_ok && m0 + j < a.M) a.Y[(int64_t)(m0 + j) * a.R + v] = float_to_bf16_bits(y[j] * col_s);
-    } else if constexpr (MODE == kLinear) {
-        float res[T];
-#pragma unroll
-        for (int j = 0; j < T; ++j)
-            res[j] = a.ep.residual && row_ok && m0 + j < a.M ? load_bf16(a.ep.residual + (int64_t)(m0 + j) * a.R + v) : 0.f;
-#pragma unroll
-        for (int j = 0; j < T; ++j)
-            if (row_ok && m0 + j < a.M)
-                a.Y[(int64_t)(m0 + j) * a.R + v] = float_to_bf16_bits(linear_epilogue(y[j], a.ep, bias, res[j]));
+            if (row_ok && m0 + j < a.M) out[(int64_t)j * a.R] = to_bf16(y[j]);
     } else {
         const int p = v & 1;
         const int64_t col = v >> 1;
         if (a.ep.GU) {
+            uint16_t* out = a.ep.GU + (int64_t)m0 * 2 * a.I + p * a.I + col;
 #pragma unroll
             for (int j = 0; j < T; ++j)
-                if (row_ok && m0 + j < a.M)
-                    a.ep.GU[(int64_t)(m0 + j) * 2 * a.I + p * a.I + col] = float_to_bf16_bits(y[j]);
+                if (row_ok && m0 + j < a.M) out[(int64_t)j * 2 * a.I] = to_bf16(y[j]);
         }
         // the even lane finishes the first half of the tokens, the odd lane the second
+        float gate[T / 2], up[T / 2];
 #pragma unroll
         for (int j = 0; j < T / 2; ++j) {
             const float got = __shfl_xor_sync(0xFFFFFFFFu, p ? y[j] : y[T / 2 + j], 1);
-            const float gate = p ? got : y[j], up = p ? y[T / 2 + j] : got;
-            const int m = m0 + (p ? T / 2 : 0) + j;
-            if (row_ok && m < a.M) a.Y[(int64_t)m * a.I + col] = float_to_bf16_bits(act_f(gate, a.ep.act) * up);
+            gate[j] = p ? got : y[j];
+            up[j] = p ? y[T / 2 + j] : got;
         }
+        act_all<T / 2>(gate, a.ep.act);
+        const int m = m0 + (p ? T / 2 : 0);
+        uint16_t* out = a.Y + (int64_t)m * a.I + col;
+#pragma unroll
+        for (int j = 0; j < T / 2; ++j)
+            if (row_ok && m + j < a.M) out[(int64_t)j * a.I] = to_bf16(gate[j] * up[j]);
     }
 }
 
@@ -770,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
         }
     } else {  // ------------------------------------------------------------------------- epilogue
         pdl_wait_primary();  // exponents come from the preparation kernels, the residual from earlier ones
-        const int quad = warp & 3;
+        const int quad = warp & 3, half = (warp - kDqWarps) >> 2;
         const int lrow = quad * 32 + lane;  // TMEM lane
         // backward: position (0,1,..,7) of every 8-block holds column (0,4,1,5,2,6,3,7)
         const int orow = kBack ? (lrow & ~7) | ((lrow & 7) >> 1) | ((lrow & 1) << 2) : lrow;
@@ -796,13 +963,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
                 if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
                 if (kBack && a.inv_s) col_s = __ldg(a.inv_s + v);
             }
-            constexpr int T = 16;
+            constexpr int T = 16, kCols = NT / 2;  // this warp's columns: kCols from half * kCols
 #pragma unroll 1
-            for (int c0 = 0; c0 < NT; c0 += T) {
+            for (int cc = 0; cc < kCols; cc += T) {
+                const int c0 = half * kCols + cc, m0 = mt * NT + c0;
+                Extra<MODE, T> x;
+                if (whole && m0 < a.M) x.load(a, m0, v);
                 uint32_t d[T];
                 tmem_ld16(tl + buf * NT + c0, d);
                 tmem_wait_ld();
-                if (c0 + T == NT) {
+                if (cc + T == kCols) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(&dfree[buf], 0);
@@ -811,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
                     float sum[T];
 #pragma unroll
                     for (int j = 0; j < T; ++j) sum[j] = __uint_as_float(d[j]);
-                    if (mt * NT + c0 < a.M) finish<MODE, T>(a, sum, mt * NT + c0, v, bias, row_e, col_s);
+                    if (m0 < a.M) finish<MODE, T>(a, sum, x, m0, v, bias, row_e, col_s);
                 } else {
 #pragma unroll
                     for (int j = 0; j < T; ++j) part[(int64_t)(c0 + j) * kTileRows] = __uint_as_float(d[j]);
@@ -843,6 +1013,8 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
     const int last = cta_of_unit((int64_t)r * a.NS + a.NS - 1, a.base, a.rem);
     if (first == last) return;  // one cluster ran the tile whole
     const int v = rt * kTileRows + threadIdx.x;
+    Extra<MODE, T> x;
+    x.load(a, mt * NT + c0, v);
     float sum[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) sum[j] = 0.f;
@@ -860,7 +1032,7 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
         if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
         if (MODE == kDx && a.inv_s) col_s = __ldg(a.inv_s + v);
     }
-    finish<MODE, T>(a, sum, mt * NT + c0, v, bias, row_e, col_s);
+    finish<MODE, T>(a, sum, x, mt * NT + c0, v, bias, row_e, col_s);
 }
 
 // ------------------------------------------------------------------ host
@@ -872,7 +1044,7 @@ int tile_tokens(int64_t M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
 struct Layout {
     int64_t Rp, Cp, Mp;
-    size_t meta, exps, texp, op, partial, total;  // byte offsets after the counter area
+    size_t meta, exps, pows, texp, op, partial, total;  // byte offsets
 };
 
 Layout layout_h(int64_t M, int64_t N, int64_t K, int group, bool back, int num_sms) {
@@ -885,7 +1057,9 @@ Layout layout_h(int64_t M, int64_t N, int64_t K, int group, bool back, int num_s
     l.meta = o;
     o += up256((size_t)(K / group) * l.Rp * 4);
     l.exps = o;
-    o += up256((size_t)l.Rp * 4);
+    o += up256((size_t)l.Rp * 2);
+    l.pows = o;
+    o += back ? up256((size_t)l.Rp * 4) : 0;
     l.texp = o;
     o += up256((size_t)l.Mp * 4);
     l.op = o;
@@ -994,7 +1168,7 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     const int64_t I = e.gated ? N / 2 : 0;
     HArgs a{};
     a.meta = reinterpret_cast<uint32_t*>(ws + l.meta);
-    a.exps = reinterpret_cast<int*>(ws + l.exps);
+    a.exps = reinterpret_cast<int16_t*>(ws + l.exps);
     a.texp = reinterpret_cast<int*>(ws + l.texp);
     a.scales = scales;
     a.zeros = zeros;
@@ -1026,8 +1200,8 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     if (!ok || !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
                                (uint64_t)l.Rp * 4, kBM, group == 32 ? 2 : 1))
         return W4A16_ERR_CUDA;
-    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int*>(ws + l.exps),
-                      (int)N, (int)l.Rp, a.GQ, I};
+    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int16_t*>(ws + l.exps),
+                      nullptr, (int)N, (int)l.Rp, a.GQ, I};
     const TokenArgs t{X, xscale, reinterpret_cast<__half*>(ws + l.op), reinterpret_cast<int*>(ws + l.texp), (int)M,
                       (int)K};
     const int meta_blocks = (int)(l.Rp / kMetaRows);
@@ -1046,7 +1220,7 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     if (!fault) return W4A16_ERR_CUDA;
     HArgs a{};
     a.meta = reinterpret_cast<uint32_t*>(ws + l.meta);
-    a.exps = reinterpret_cast<int*>(ws + l.exps);
+    a.exps = reinterpret_cast<int16_t*>(ws + l.exps);
     a.texp = reinterpret_cast<int*>(ws + l.texp);
     a.scales = scales;
     a.zeros = zeros;
@@ -1073,8 +1247,8 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
         !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
                         (uint64_t)l.Rp * 4, kBK, (uint32_t)(kBM / group)))  // 64 rows x the groups of 128 columns
         return W4A16_ERR_CUDA;
-    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int*>(ws + l.exps),
-                      (int)N, (int)l.Rp, a.GQ, 0};
+    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int16_t*>(ws + l.exps),
+                      reinterpret_cast<float*>(ws + l.pows), (int)N, (int)l.Rp, a.GQ, 0};
     int st = launch_pdl(prep_meta_kernel, l.Rp / kMetaRows, kPrepThreads, stream, ma);
     if (st != W4A16_OK) return st;
     GradArgs g{};
@@ -1083,6 +1257,7 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     g.GU = GU;
     g.dGU = dGU;
     g.exps = a.exps;
+    g.pows = reinterpret_cast<float*>(ws + l.pows);
     g.Dh = reinterpret_cast<__half*>(ws + l.op);
     g.texp = reinterpret_cast<int*>(ws + l.texp);
     g.N = (int)N;
@@ -1091,11 +1266,11 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     g.Np = l.Cp;
     // 16-byte loads where every row (gated: every half row) of the inputs starts on a 16-byte boundary
     if (dH)
-        st = g.I % 8 == 0 ? launch_pdl(prep_grad_kernel<8, true>, M, kGradThreads, stream, g)
-                          : launch_pdl(prep_grad_kernel<1, true>, M, kGradThreads, stream, g);
+        st = g.I % 8 == 0 ? launch_pdl(prep_grad_kernel<true, true>, M, kGradThreads, stream, g)
+                          : launch_pdl(prep_grad_kernel<false, true>, M, kGradThreads, stream, g);
     else
-        st = N % 8 == 0 ? launch_pdl(prep_grad_kernel<8, false>, M, kGradThreads, stream, g)
-                        : launch_pdl(prep_grad_kernel<1, false>, M, kGradThreads, stream, g);
+        st = N % 8 == 0 ? launch_pdl(prep_grad_kernel<true, false>, M, kGradThreads, stream, g)
+                        : launch_pdl(prep_grad_kernel<false, false>, M, kGradThreads, stream, g);
     if (st != W4A16_OK) return st;
     return launch_mode<kDx>(NT, a, tx, tq, tm, stream);
 }
