@@ -15,7 +15,8 @@ namespace {
 
 constexpr int kEpThreads = 256;
 constexpr int kEpRows = 128;   // rows per slot
-constexpr int kCcLoads = 32;   // slot loads in flight per thread
+template <int H>
+constexpr int kCcLoads = 32 / H;  // slot loads in flight per thread (with 32 registers; the gated kernel holds more state)
 
 struct CcSlots {
     const float* partial;
@@ -24,8 +25,9 @@ struct CcSlots {
 
 // One token.  An item is R = 256 / (H P) outputs; H = 2 for the gated product (the output's gate row and up row
 // are summed by different threads), P threads share a row's slots (part p takes slots p, p + P, ...).
+// At most 32 registers, so that its CTAs fit beside the four GEMV CTAs of an SM and wait there.
 template <int P, int H>
-__global__ void __launch_bounds__(kEpThreads) cc_epilogue_kernel(const CcSlots c, const FusedEpilogue e,
+__global__ void __launch_bounds__(kEpThreads, 8) cc_epilogue_kernel(const CcSlots c, const FusedEpilogue e,
                                                                  uint16_t* Y, int outs) {
     constexpr int R = kEpThreads / (P * H);
     __shared__ float s_part[P * H][R];
@@ -44,15 +46,15 @@ __global__ void __launch_bounds__(kEpThreads) cc_epilogue_kernel(const CcSlots c
                                       : (int64_t)c.tiles_a * c.cpt + (int64_t)(tile - c.tiles_a) * c.cpt_b;
             const int nslots = tile < c.tiles_a ? c.cpt : c.cpt_b;
             const float* pb = c.partial + first * kEpRows + n % kEpRows;
-            for (int k0 = p; k0 < nslots; k0 += kCcLoads * P) {
-                float v[kCcLoads];
+            for (int k0 = p; k0 < nslots; k0 += kCcLoads<H> * P) {
+                float v[kCcLoads<H>];
 #pragma unroll
-                for (int i = 0; i < kCcLoads; ++i) {
+                for (int i = 0; i < kCcLoads<H>; ++i) {
                     const int k = k0 + i * P;
                     v[i] = k < nslots ? __ldcg(pb + (int64_t)k * kEpRows) : 0.f;
                 }
 #pragma unroll
-                for (int i = 0; i < kCcLoads; ++i) acc += v[i];
+                for (int i = 0; i < kCcLoads<H>; ++i) acc += v[i];
             }
         }
         s_part[q][r] = acc;
@@ -153,7 +155,7 @@ int launch_cc_epilogue(const float* partial, const FusedEpilogue& e, uint16_t* Y
     const CcSlots c{partial, cpt, tiles_a, cpt_b};
     // four parts where a row has more slots than two parts load in one round trip; at most one CTA per SM, so
     // that the next call's GEMV CTAs find their places
-    const bool four = (cpt > cpt_b ? cpt : cpt_b) > 2 * kCcLoads;
+    const bool four = (cpt > cpt_b ? cpt : cpt_b) > (e.gated ? 2 * kCcLoads<2> : 2 * kCcLoads<1>);
     const int outs = (int)(e.gated ? N / 2 : N);
     const int R = kEpThreads / ((four ? 4 : 2) * (e.gated ? 2 : 1));
     const int64_t items = ceil_div(outs, R), grid = items < sms ? items : sms;

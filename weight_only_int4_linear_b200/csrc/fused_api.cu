@@ -51,12 +51,14 @@ int forward_entry(const uint16_t* X, const float* inv_s, int64_t M, int64_t K, i
         return W4A16_ERR_ALIGN;
     if ((st = check_device()) != W4A16_OK) return st;
     const Path p = forward_path(M, K, group, inv_s != nullptr);
-    if (!workspace || workspace_bytes < path_bytes(p, M, N, K, group)) return W4A16_ERR_WORKSPACE;
+    DecodePlan plan{};
+    if (p == kCc || p == kMt) plan = plan_decode(M, N, K, num_sms_current());
+    const size_t need = p == kCc || p == kMt ? plan.workspace_bytes() : path_bytes(p, M, N, K, group);
+    if (!workspace || workspace_bytes < need) return W4A16_ERR_WORKSPACE;
     if (misaligned(workspace)) return W4A16_ERR_ALIGN;
     cudaStream_t s = (cudaStream_t)stream;
     if (p == kGemm) return launch_gemm_h(X, inv_s, M, K, group, qweight, scales, zeros, N, e, Y, workspace, s);
     if (p == kSub) return launch_decode_sub(X, M, K, group, qweight, scales, zeros, N, Y, workspace, s, &e);
-    const DecodePlan plan = plan_decode(M, N, K, num_sms_current());
     return launch_decode(X, inv_s, M, K, qweight, scales, zeros, N, Y, workspace, plan, s, nullptr, nullptr, &e);
 }
 

@@ -136,15 +136,15 @@ __device__ __forceinline__ int64_t gated_row(int64_t v, int64_t I) { return (v &
 // half: the dequantiser then forms the value in binary64 from the stored scale and zero point.  Rows past the
 // matrix get zero words (s' = 0).  exps[v] = e of row v.
 constexpr int kPrepThreads = 256;
-constexpr int kMetaRows = kPrepThreads / 32;  // rows per block: a warp each (8 words of a line: one 32-byte sector)
-constexpr int kMetaChunk = 128;               // groups per step: four loads in flight per lane
+constexpr int kMetaRows = 32;   // rows per block, four per warp: their loads are in flight together
+constexpr int kMetaGroups = 256;  // groups held in shared memory at a time
 
 struct MetaArgs {
     const uint16_t* scales;
     const int32_t* zeros;
     uint32_t* meta;
     int16_t* exps;  // [Rp] e
-    float* pows;    // [Rp] 2^e (backward), 0 where it is no normal FP32 number
+    uint8_t* pows;  // [Rp] e + 127 (backward): the FP32 exponent field of 2^e, 0 where that is no normal number
     int R, Rp, GQ;
     int64_t I;      // gated: rows per half, else 0
 };
@@ -155,58 +155,76 @@ __device__ __forceinline__ int bf16_exponent(uint32_t bits) {  // floor(log2 |x|
 }
 constexpr int kNothing = -100000;  // exponent of zero
 
+// Rows of up to 256 groups are read once: scale and zero point wait in shared memory for the row's exponent.
 __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
-    __shared__ uint32_t s_word[kMetaRows][kMetaChunk + 1];
+    __shared__ uint32_t s_raw[kMetaRows][kMetaGroups + 1];  // scale bits, zero point << 16 (0x7FFF: beyond 1024)
+    __shared__ int s_exp[kMetaRows];
+    constexpr int RW = kMetaRows / (kPrepThreads / 32);  // rows per warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int v0 = block * kMetaRows, v = v0 + warp;
-    const bool row_ok = v < a.R;
-    const int64_t n = row_ok ? (a.I ? gated_row(v, a.I) : v) : 0;
-    const uint16_t* sc = a.scales + n * a.GQ;
-    const int32_t* ze = a.zeros + n * a.GQ;
-    constexpr int L = kMetaChunk / 32;
-    int top = kNothing;
-    for (int g0 = 0; g0 < a.GQ; g0 += kMetaChunk) {
-        uint32_t sb[L];
-        int z[L];
+    const int v0 = block * kMetaRows, r0 = warp * RW;
+    int64_t first[RW];  // the row's first group, -1 past the matrix
+    int top[RW];
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int g = g0 + 32 * i + lane;
-            const bool ok = row_ok && g < a.GQ;
-            sb[i] = ok ? __ldg(sc + g) : 0u;
-            z[i] = ok ? __ldg(ze + g) : 0;
+    for (int i = 0; i < RW; ++i) {
+        const int v = v0 + r0 + i;
+        first[i] = v < a.R ? (a.I ? gated_row(v, a.I) : (int64_t)v) * a.GQ : -1;
+        top[i] = kNothing;
+    }
+    // groups g0 .. g1 - 1 of the warp's rows into shared memory, two groups of four rows in flight per lane
+    auto read = [&](int g0, int g1) {
+        for (int gb = g0; gb < g1; gb += 64) {
+            uint32_t sb[RW][2];
+            int z[RW][2];
+#pragma unroll
+            for (int i = 0; i < RW; ++i)
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    const int g = gb + 32 * l + lane;
+                    const bool ok = first[i] >= 0 && g < g1;
+                    sb[i][l] = ok ? __ldg(a.scales + first[i] + g) : 0u;
+                    z[i][l] = ok ? __ldg(a.zeros + first[i] + g) : 0;
+                }
+#pragma unroll
+            for (int i = 0; i < RW; ++i)
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    const int g = gb + 32 * l + lane, zz = z[i][l];
+                    // |q - z| <= max(|z|, |15 - z|) < 2^bits, |s| < 2^(exponent + 1)
+                    const uint32_t mag = zz < 8 ? 15u - (uint32_t)zz : (uint32_t)zz;
+                    if (sb[i][l] & 0x7FFFu) top[i] = max(top[i], bf16_exponent(sb[i][l]) + 1 + (32 - __clz(mag)));
+                    const uint32_t zw = zz >= -1024 && zz <= 1024 ? (uint32_t)zz & 0xFFFFu : 0x7FFFu;
+                    if (g < g1) s_raw[r0 + i][g - g0] = sb[i][l] | (zw << 16);
+                }
         }
+    };
+    for (int g0 = 0; g0 < a.GQ; g0 += kMetaGroups) read(g0, min(g0 + kMetaGroups, a.GQ));
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            // |q - z| <= max(|z|, |15 - z|) < 2^bits, |s| < 2^(exponent + 1)
-            const uint32_t mag = z[i] < 8 ? 15u - (uint32_t)z[i] : (uint32_t)z[i];
-            if (sb[i] & 0x7FFFu) top = max(top, bf16_exponent(sb[i]) + 1 + (32 - __clz(mag)));
+    for (int i = 0; i < RW; ++i) {
+        const int t = __reduce_max_sync(0xFFFFFFFFu, top[i]), e = t == kNothing ? 0 : t - kTopExp;
+        if (lane == 0) {
+            const int v = v0 + r0 + i;
+            s_exp[r0 + i] = e;
+            a.exps[v] = (int16_t)e;
+            if (a.pows) a.pows[v] = (uint8_t)(e >= -126 && e <= 127 ? e + 127 : 0);
         }
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    const int e = top == kNothing ? 0 : top - kTopExp;
-    if (lane == 0) {
-        a.exps[v] = (int16_t)e;
-        if (a.pows) a.pows[v] = e >= -126 && e <= 127 ? __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
-    }
-    for (int g0 = 0; g0 < a.GQ; g0 += kMetaChunk) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int g = g0 + 32 * i + lane;
-            uint32_t word = 0;
-            if (row_ok && g < a.GQ) {
-                const int z = __ldg(ze + g);
-                const float s = scale2(bf16_bits_to_float(__ldg(sc + g)), -e);
-                word = z >= -1024 && z <= 1024 ? (uint32_t)__half_as_ushort(__float2half_rn(s)) |
-                                                     ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16)
-                                               : ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
-            }
-            s_word[warp][32 * i + lane] = word;
+    for (int g0 = 0; g0 < a.GQ; g0 += kMetaGroups) {
+        const int g1 = min(g0 + kMetaGroups, a.GQ);
+        if (a.GQ > kMetaGroups) {
+            __syncthreads();  // the preceding words are out
+            read(g0, g1);
         }
         __syncthreads();
-        const int r = threadIdx.x % kMetaRows;
-        for (int g = threadIdx.x / kMetaRows; g < min(kMetaChunk, a.GQ - g0); g += kPrepThreads / kMetaRows)
-            a.meta[(int64_t)(g0 + g) * a.Rp + v0 + r] = s_word[r][g];
-        __syncthreads();
+        const int e = s_exp[lane];  // lane: the row
+        for (int g = warp; g < g1 - g0; g += kPrepThreads / 32) {
+            const uint32_t raw = s_raw[lane][g];
+            const int z = (int)raw >> 16;
+            const float s = scale2(bf16_bits_to_float((uint16_t)raw), -e);
+            const uint32_t word = z != 0x7FFF ? (uint32_t)__half_as_ushort(__float2half_rn(s)) |
+                                                    ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16)
+                                              : ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
+            a.meta[(int64_t)(g0 + g) * a.Rp + v0 + lane] = v0 + lane < a.R ? word : 0u;
+        }
     }
 }
 
@@ -261,17 +279,24 @@ __global__ void __launch_bounds__(kPrepThreads) prep_forward_kernel(const MetaAr
         }
         return v;
     };
-    uint32_t top = 0;  // largest magnitude as BF16 bits
-    for (int i = threadIdx.x; i < n8; i += kPrepThreads) {
-        const uint4 v = load(i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr int U = 4;  // loads in flight per thread
+    uint32_t top = 0;     // largest magnitude as BF16 bits
+    for (int i0 = threadIdx.x; i0 < n8; i0 += U * kPrepThreads) {
+        uint4 v[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+        for (int u = 0; u < U; ++u) v[u] = i0 + u * kPrepThreads < n8 ? load(i0 + u * kPrepThreads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+        }
     }
     const int a = row_exp(block_max(top ? bf16_exponent(top) : kNothing));
     const int h = -a >> 1;
     const float f1 = pow2f(h), f2 = pow2f(-a - h);  // |a| <= 150: both factors are FP32 powers of two
     if (threadIdx.x == 0) t.texp[m] = a;
+#pragma unroll 4
     for (int i = threadIdx.x; i < n8; i += kPrepThreads) {
         const uint4 v = load(i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -308,7 +333,7 @@ struct GradArgs {
     const uint16_t* GU;
     uint16_t* dGU;
     const int16_t* exps;  // [>= N] e_n
-    const float* pows;    // [>= N] 2^e_n, or 0
+    const uint8_t* pows;  // [>= N] exponent field of 2^e_n, or 0
     __half* Dh;
     int* texp;
     int N, I, act;
@@ -338,14 +363,15 @@ struct Lane8 {
             for (int j = 0; j < 8; ++j) f[j] = at(i, j) < n ? bf16_bits_to_float(p[at(i, j)]) : 0.f;
         }
     }
-    __device__ __forceinline__ static void load(const float* p, int i, int n, bool vec, float (&f)[8]) {
-        if (VEC && vec) {
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(p + i)), b = __ldcg(reinterpret_cast<const float4*>(p + i + 4));
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    // powers of two from their exponent fields; 1 past the row
+    __device__ __forceinline__ static void load_pows(const uint8_t* p, int i, int n, float (&f)[8]) {
+        if constexpr (VEC) {
+            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p + i));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float((((j < 4 ? v.x : v.y) >> (8 * (j & 3))) & 0xFFu) << 23);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = at(i, j) < n ? __ldcg(p + at(i, j)) : 1.f;
+            for (int j = 0; j < 8; ++j) f[j] = at(i, j) < n ? __uint_as_float((uint32_t)__ldcg(p + at(i, j)) << 23) : 1.f;
         }
     }
     __device__ __forceinline__ static void load(const int16_t* p, int i, int n, int (&e)[8]) {
@@ -408,12 +434,12 @@ __global__ void __launch_bounds__(kGradThreads, 2) prep_grad_kernel(const GradAr
         if (i >= n) break;
         float d[8], p[8];
         L::load(d0, i, n, d);
-        L::load(g.pows, i, n, true, p);
+        L::load_pows(g.pows, i, n, p);
         if constexpr (GATED) {
             float gg[8], uu[8], q[8];
             L::load(gu, i, n, gg);
             L::load(gu + g.I, i, n, uu);
-            L::load(g.pows + g.I, i, n, true, q);
+            L::load_pows(g.pows + g.I, i, n, q);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 bound = fmaxf(bound, fmaxf(fabsf(2.f * d[j] * uu[j]) * p[j], fabsf(d[j] * gg[j]) * q[j]));
@@ -463,7 +489,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) prep_grad_kernel(const GradAr
             float v[8], u[8], p[8];
             values(i, v, u);
             if constexpr (GATED) L::store_bf(dgu, i, n, v);
-            L::load(g.pows, i, n, true, p);
+            L::load_pows(g.pows, i, n, p);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[j] = v[j] * p[j] * fa;
@@ -472,7 +498,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) prep_grad_kernel(const GradAr
             L::store_half(out, i, n, v);
             if constexpr (GATED) {
                 L::store_bf(dgu + g.I, i, n, u);
-                L::load(g.pows + g.I, i, n, true, p);
+                L::load_pows(g.pows + g.I, i, n, p);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     u[j] = u[j] * p[j] * fa;
@@ -781,13 +807,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
             prefetch_tmap(toks ? &tx : &tq);
             if (!toks) prefetch_tmap(&tm);
         }
-        pdl_wait_primary();  // operands and meta words come from the preparation kernels
         Ring<S> r;
         int issued = 0;
         bool ok = true;
         const int lg = a.group >> 6;  // log2(group / 32): 0, 1, 2
         const int lines = kBack ? kBM / a.group : (lg == 0 ? 2 : 1);
         const uint32_t bytes = toks ? C::kXBytes : kCodeBytes + lines * (kBack ? kBK : kBM) * 4;
+        pdl_wait_primary();  // operands and meta words come from the preparation kernels
         while (ok && seg.next(a)) {
             int rt, mt;
             tile_coords(seg.tile, a, rt, mt);
@@ -1018,12 +1044,21 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
     float sum[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) sum[j] = 0.f;
-    for (int b = first; b <= last; ++b) {
+    const int64_t u0 = (int64_t)r * a.NS;  // the tile's first stage
+    auto part = [&](int b) {
         const int64_t u = (int64_t)b * a.base + min(b, a.rem);  // the cluster's first stage
-        const int s0 = (int)max(u - (int64_t)r * a.NS, (int64_t)0);
-        const float* p = a.partial + ((int64_t)slot_of(b, s0) * NT + c0) * kTileRows + threadIdx.x;
+        return a.partial + ((int64_t)slot_of(b, u > u0 ? 1 : 0) * NT + c0) * kTileRows + threadIdx.x;
+    };
+    for (int b = first; b <= last; b += 2) {  // two parts' loads in flight
+        const float *p = part(b), *q = part(min(b + 1, last));
+        float f[T], g[T];
 #pragma unroll
-        for (int j = 0; j < T; ++j) sum[j] += __ldcg(p + j * kTileRows);
+        for (int j = 0; j < T; ++j) {
+            f[j] = __ldcg(p + j * kTileRows);
+            g[j] = b < last ? __ldcg(q + j * kTileRows) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < T; ++j) sum[j] = sum[j] + f[j] + g[j];
     }
     float bias = 0.f, col_s = 1.f;
     int row_e = 0;
@@ -1059,13 +1094,13 @@ Layout layout_h(int64_t M, int64_t N, int64_t K, int group, bool back, int num_s
     l.exps = o;
     o += up256((size_t)l.Rp * 2);
     l.pows = o;
-    o += back ? up256((size_t)l.Rp * 4) : 0;
+    o += back ? up256((size_t)l.Rp) : 0;
     l.texp = o;
     o += up256((size_t)l.Mp * 4);
     l.op = o;
     o += up256((size_t)M * l.Cp * 2);
     l.partial = o;
-    o += (size_t)(num_sms / 2) * 2 * NT * kTileRows * 4;
+    o += (size_t)(num_sms / 2) * 2 * NT * kTileRows * 4;  // two slots per CTA pair
     l.total = o;
     return l;
 }
@@ -1196,7 +1231,7 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
                                              {kBK / 8, 2, kBM / 2}, CU_TENSOR_MAP_SWIZZLE_32B)
                             : encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N,
                                              (uint64_t)K / 2, kBK / 8, kBM, CU_TENSOR_MAP_SWIZZLE_32B);
-    // the meta words of a stage: 128 rows x the groups of its 64 k
+    // the meta words of a stage: its rows x the groups of its 64 k
     if (!ok || !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
                                (uint64_t)l.Rp * 4, kBM, group == 32 ? 2 : 1))
         return W4A16_ERR_CUDA;
@@ -1239,16 +1274,17 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     a.m_tiles = (int)ceil_div(M, NT);
     a.r_tiles = (int)ceil_div(K, kTileRows);
     CUtensorMap tx, tq, tm;
-    // rows of N values, Np apart: what lies past N is filled with zeros
+    // rows of N values, Np apart: what lies past N is filled with zeros.  Codes: 64 rows x the columns; meta words: 64
+    // rows x the columns' groups.
     if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + l.op, (uint64_t)N, (uint64_t)M, (uint64_t)l.Cp * 2,
                         kBK, (uint32_t)NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N, (uint64_t)K / 2,
                         kBM / 8, kBK, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
-                        (uint64_t)l.Rp * 4, kBK, (uint32_t)(kBM / group)))  // 64 rows x the groups of 128 columns
+                        (uint64_t)l.Rp * 4, kBK, (uint32_t)(kBM / group)))
         return W4A16_ERR_CUDA;
     const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int16_t*>(ws + l.exps),
-                      reinterpret_cast<float*>(ws + l.pows), (int)N, (int)l.Rp, a.GQ, 0};
+                      reinterpret_cast<uint8_t*>(ws + l.pows), (int)N, (int)l.Rp, a.GQ, 0};
     int st = launch_pdl(prep_meta_kernel, l.Rp / kMetaRows, kPrepThreads, stream, ma);
     if (st != W4A16_OK) return st;
     GradArgs g{};
@@ -1257,7 +1293,7 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     g.GU = GU;
     g.dGU = dGU;
     g.exps = a.exps;
-    g.pows = reinterpret_cast<float*>(ws + l.pows);
+    g.pows = reinterpret_cast<uint8_t*>(ws + l.pows);
     g.Dh = reinterpret_cast<__half*>(ws + l.op);
     g.texp = reinterpret_cast<int*>(ws + l.texp);
     g.N = (int)N;
