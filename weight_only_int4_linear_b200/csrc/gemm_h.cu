@@ -163,12 +163,14 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int v0 = block * kMetaRows, r0 = warp * RW;
     int64_t first[RW];  // the row's first group, -1 past the matrix
-    int top[RW];
+    int top[RW];         // exponent bound of the row's values: |s| < 2^(exponent + 1) times the zero point's part
+    uint32_t usual[RW];  // largest scale of the groups with a zero point in 0 .. 15, where |q - z| < 2^4
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
         const int v = v0 + r0 + i;
         first[i] = v < a.R ? (a.I ? gated_row(v, a.I) : (int64_t)v) * a.GQ : -1;
         top[i] = kNothing;
+        usual[i] = 0u;
     }
     // groups g0 .. g1 - 1 of the warp's rows into shared memory, two groups of four rows in flight per lane
     auto read = [&](int g0, int g1) {
@@ -189,17 +191,23 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
 #pragma unroll
                 for (int l = 0; l < 2; ++l) {
                     const int g = gb + 32 * l + lane, zz = z[i][l];
-                    // |q - z| <= max(|z|, |15 - z|) < 2^bits, |s| < 2^(exponent + 1)
-                    const uint32_t mag = zz < 8 ? 15u - (uint32_t)zz : (uint32_t)zz;
-                    if (sb[i][l] & 0x7FFFu) top[i] = max(top[i], bf16_exponent(sb[i][l]) + 1 + (32 - __clz(mag)));
-                    const uint32_t zw = zz >= -1024 && zz <= 1024 ? (uint32_t)zz & 0xFFFFu : 0x7FFFu;
-                    if (g < g1) s_raw[r0 + i][g - g0] = sb[i][l] | (zw << 16);
+                    if (g >= g1) continue;
+                    uint32_t zw = (uint32_t)zz << 16;
+                    if ((uint32_t)zz < 16u) {
+                        usual[i] = max(usual[i], sb[i][l] & 0x7FFFu);
+                    } else {  // |q - z| <= max(|z|, |15 - z|) < 2^bits
+                        const uint32_t mag = zz < 8 ? 15u - (uint32_t)zz : (uint32_t)zz;
+                        if (sb[i][l] & 0x7FFFu) top[i] = max(top[i], bf16_exponent(sb[i][l]) + 1 + (32 - __clz(mag)));
+                        if (zz < -1024 || zz > 1024) zw = 0x7FFF0000u;
+                    }
+                    s_raw[r0 + i][g - g0] = sb[i][l] | zw;
                 }
         }
     };
     for (int g0 = 0; g0 < a.GQ; g0 += kMetaGroups) read(g0, min(g0 + kMetaGroups, a.GQ));
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
+        if (usual[i]) top[i] = max(top[i], bf16_exponent(usual[i]) + 1 + 4);
         const int t = __reduce_max_sync(0xFFFFFFFFu, top[i]), e = t == kNothing ? 0 : t - kTopExp;
         if (lane == 0) {
             const int v = v0 + r0 + i;
@@ -216,14 +224,23 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
         }
         __syncthreads();
         const int e = s_exp[lane];  // lane: the row
-        for (int g = warp; g < g1 - g0; g += kPrepThreads / 32) {
+        // A positive scale whose 2^-e multiple is a normal FP16 number, and a zero point in 0 .. 1023: the word by
+        // integer arithmetic on the formats' fields (exponent bias 127 -> 15, 7 -> 10 mantissa bits; 1024 + z is
+        // 0x6400 + z).  Else by conversions.
+        const int bias = (15 - 127 - e) * 1024;
+        uint32_t* out = a.meta + (int64_t)(g0 + warp) * a.Rp + v0 + lane;
+        for (int g = warp; g < g1 - g0; g += kPrepThreads / 32, out += (int64_t)(kPrepThreads / 32) * a.Rp) {
             const uint32_t raw = s_raw[lane][g];
-            const int z = (int)raw >> 16;
-            const float s = scale2(bf16_bits_to_float((uint16_t)raw), -e);
-            const uint32_t word = z != 0x7FFF ? (uint32_t)__half_as_ushort(__float2half_rn(s)) |
-                                                    ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16)
-                                              : ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
-            a.meta[(int64_t)(g0 + g) * a.Rp + v0 + lane] = v0 + lane < a.R ? word : 0u;
+            const int h = (int)((raw & 0xFFFFu) << 3) + bias;
+            uint32_t word = (uint32_t)h + (raw & 0xFFFF0000u) + 0x64000000u;
+            if (h < 0x400 || h > 0x7BFF || (raw & 0x8000u) || raw >= (1024u << 16)) {
+                const int z = (int)raw >> 16;
+                const float s = scale2(bf16_bits_to_float((uint16_t)raw), -e);
+                word = z != 0x7FFF ? (uint32_t)__half_as_ushort(__float2half_rn(s)) |
+                                         ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16)
+                                   : ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
+            }
+            *out = v0 + lane < a.R ? word : 0u;
         }
     }
 }
@@ -256,16 +273,15 @@ struct TokenArgs {
     int M, K;
 };
 
-// Forward preparation: the first meta_blocks blocks write the weights' meta words, the others one token each.
-__global__ void __launch_bounds__(kPrepThreads) prep_forward_kernel(const MetaArgs ma, int meta_blocks,
-                                                                    const TokenArgs t) {
+// Forward preparation: the first M blocks take a token each, the others the weights' meta words.
+__global__ void __launch_bounds__(kPrepThreads) prep_forward_kernel(const MetaArgs ma, const TokenArgs t) {
     pdl_launch_dependents();
     pdl_wait_primary();  // X of an earlier kernel; the workspace's earlier readers
-    if ((int)blockIdx.x < meta_blocks) {
-        meta_block(ma, blockIdx.x);
+    const int m = blockIdx.x;
+    if (m >= t.M) {
+        meta_block(ma, m - t.M);
         return;
     }
-    const int m = blockIdx.x - meta_blocks;
     const uint4* x = reinterpret_cast<const uint4*>(t.X + (int64_t)m * t.K);
     uint4* out = reinterpret_cast<uint4*>(t.Xh + (int64_t)m * t.K);
     const int n8 = t.K / 8;
@@ -1240,7 +1256,7 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     const TokenArgs t{X, xscale, reinterpret_cast<__half*>(ws + l.op), reinterpret_cast<int*>(ws + l.texp), (int)M,
                       (int)K};
     const int meta_blocks = (int)(l.Rp / kMetaRows);
-    const int st = launch_pdl(prep_forward_kernel, meta_blocks + M, kPrepThreads, stream, ma, meta_blocks, t);
+    const int st = launch_pdl(prep_forward_kernel, meta_blocks + M, kPrepThreads, stream, ma, t);
     if (st != W4A16_OK) return st;
     return e.gated ? launch_mode<kGated>(NT, a, tx, tq, tm, stream) : launch_mode<kLinear>(NT, a, tx, tq, tm, stream);
 }
