@@ -262,51 +262,44 @@ def dx_workspace_bytes(M: int, N: int, K: int, group: int = GROUP) -> int:
     return int(load().w4a16_dx_workspace_bytes(M, N, K, group))
 
 
-class _On:
-    """Marshals tensors that must share one CUDA device; `call` runs with that device current, on `stream` (None:
-    the device's current stream)."""
+def _ok(t, dtype, index: int, shape) -> bool:
+    """A contiguous CUDA tensor of this type and shape on device `index`."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape
+            and t.is_contiguous())
 
-    __slots__ = ("device", "index")
 
-    def __init__(self, t: torch.Tensor, name: str):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        self.device, self.index = t.device, t.get_device()
+def _refuse(tensors, index: int) -> None:
+    """Says what is wrong with the first tensor that _ok turned down; tensors: (tensor, name, dtype, shape)."""
+    for t, name, dtype, shape in tensors:
+        _dev(t, name, dtype, shape)
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
+    raise ValueError("the tensors do not fit together")
 
-    def ptr(self, t, name: str, dtype, shape=None) -> int:
-        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == self.index >= 0
-                and t.is_contiguous() and (shape is None or t.shape == shape)):
-            return t.data_ptr()
-        _dev(t, name, dtype, shape)  # says what is wrong with it
-        raise ValueError(f"{name} must be on {self.device}, is on {t.device}")
 
-    def opt(self, t, name: str, dtype, shape):
-        return None if t is None else self.ptr(t, name, dtype, shape)
-
-    def weight(self, qweight, scales, zeros, N: int, K: int, group: int):
-        if group not in (32, 64, 128):
-            raise ValueError("group must be 32, 64 or 128")
-        return (self.ptr(qweight, "qweight", torch.int32, (N, K // 8)),
-                self.ptr(scales, "scales", torch.bfloat16, (N, K // group)),
-                self.ptr(zeros, "zeros", torch.int32, (N, K // group)))
-
-    def call(self, name: str, stream, *args) -> None:
-        if isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
-            raise ValueError(f"stream must be on {self.device}, is on {stream.device}")
-        fn = getattr(load(), name)
-        if self.index == torch.cuda.current_device():
+def _call(name: str, index: int, stream, *args) -> None:
+    """The library call with device `index` current, on `stream` (None: that device's current stream)."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+        raise ValueError(f"stream must be on cuda:{index}, is on {stream.device}")
+    fn = getattr(_lib or load(), name)
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(index):
             st = fn(*args, _stream(stream))
-        else:
-            with torch.cuda.device(self.device):
-                st = fn(*args, _stream(stream))
-        if st != OK:
-            _check(name, st)
+    if st != OK:
+        _check(name, st)
 
 
-def _two_dims(t: torch.Tensor, name: str):
+def _two_dims(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     return t.shape
+
+
+_BF, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
 
 def linear_fused(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, Y: torch.Tensor,
@@ -315,13 +308,22 @@ def linear_fused(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, z
                  stream=None) -> None:
     """w4a16_linear_fused: Y[M, N] = act(X[M, K] . W_hat^T + bias) + residual (residual may be Y itself); with inv_s,
     X is first replaced by bf16(X * inv_s).  workspace: zeroed once, >= fused_workspace_bytes(M, N, K, group)."""
-    on = _On(X, "X")
     M, K = _two_dims(X, "X")
     N = qweight.shape[0]
-    on.call("w4a16_linear_fused", stream, on.ptr(X, "X", torch.bfloat16), on.opt(inv_s, "inv_s", torch.float32, (K,)),
-            M, K, group, *on.weight(qweight, scales, zeros, N, K, group), N,
-            on.opt(bias, "bias", torch.bfloat16, (N,)), act, on.opt(residual, "residual", torch.bfloat16, (M, N)),
-            on.ptr(Y, "Y", torch.bfloat16, (M, N)), on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    i, meta = X.get_device(), (N, K // group)
+    if not (_ok(X, _BF, i, (M, K)) and _ok(qweight, _I32, i, (N, K // 8)) and _ok(scales, _BF, i, meta)
+            and _ok(zeros, _I32, i, meta) and _ok(Y, _BF, i, (M, N)) and _ok(workspace, _U8, i, workspace.shape)
+            and (bias is None or _ok(bias, _BF, i, (N,))) and (residual is None or _ok(residual, _BF, i, (M, N)))
+            and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
+        _refuse([(X, "X", _BF, (M, K)), (qweight, "qweight", _I32, (N, K // 8)), (scales, "scales", _BF, meta),
+                 (zeros, "zeros", _I32, meta), (Y, "Y", _BF, (M, N)), (workspace, "workspace", _U8, None)]
+                + [(t, n, d, s) for t, n, d, s in [(bias, "bias", _BF, (N,)), (residual, "residual", _BF, (M, N)),
+                                                   (inv_s, "inv_s", _F32, (K,))] if t is not None], i)
+    _call("w4a16_linear_fused", i, stream, X.data_ptr(), None if inv_s is None else inv_s.data_ptr(), M, K, group,
+          qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, None if bias is None else bias.data_ptr(), act,
+          None if residual is None else residual.data_ptr(), Y.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def gated(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, H: torch.Tensor,
@@ -329,27 +331,43 @@ def gated(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: t
           inv_s: torch.Tensor | None = None, stream=None) -> None:
     """w4a16_gated: H[M, I] = act(G) * U with [G | U] = X . W_hat^T, the packed weight holding I gate rows and then I
     up rows; GU [M, 2 I] receives [G | U] when given (gated_backward needs it)."""
-    on = _On(X, "X")
     M, K = _two_dims(X, "X")
     N = qweight.shape[0]
     if N % 2:
         raise ValueError("a gated weight has an even number of rows")
-    on.call("w4a16_gated", stream, on.ptr(X, "X", torch.bfloat16), on.opt(inv_s, "inv_s", torch.float32, (K,)), M, K,
-            group, *on.weight(qweight, scales, zeros, N, K, group), N, act,
-            on.ptr(H, "H", torch.bfloat16, (M, N // 2)), on.opt(GU, "GU", torch.bfloat16, (M, N)),
-            on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    i, meta = X.get_device(), (N, K // group)
+    if not (_ok(X, _BF, i, (M, K)) and _ok(qweight, _I32, i, (N, K // 8)) and _ok(scales, _BF, i, meta)
+            and _ok(zeros, _I32, i, meta) and _ok(H, _BF, i, (M, N // 2)) and _ok(workspace, _U8, i, workspace.shape)
+            and (GU is None or _ok(GU, _BF, i, (M, N))) and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
+        _refuse([(X, "X", _BF, (M, K)), (qweight, "qweight", _I32, (N, K // 8)), (scales, "scales", _BF, meta),
+                 (zeros, "zeros", _I32, meta), (H, "H", _BF, (M, N // 2)), (workspace, "workspace", _U8, None)]
+                + [(t, n, d, s) for t, n, d, s in [(GU, "GU", _BF, (M, N)), (inv_s, "inv_s", _F32, (K,))]
+                   if t is not None], i)
+    _call("w4a16_gated", i, stream, X.data_ptr(), None if inv_s is None else inv_s.data_ptr(), M, K, group,
+          qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, act, H.data_ptr(),
+          None if GU is None else GU.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def linear_dx(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, dX: torch.Tensor,
               workspace: torch.Tensor, group: int = GROUP, inv_s: torch.Tensor | None = None, stream=None) -> None:
     """w4a16_linear_dx: dX[M, K] = dY[M, N] . W_hat (times inv_s per column when given), the gradient of the layer's
     input.  workspace: >= dx_workspace_bytes(M, N, K, group)."""
-    on = _On(dY, "dY")
     M, N = _two_dims(dY, "dY")
     K = qweight.shape[1] * 8
-    on.call("w4a16_linear_dx", stream, on.ptr(dY, "dY", torch.bfloat16), M, N, group,
-            *on.weight(qweight, scales, zeros, N, K, group), K, on.opt(inv_s, "inv_s", torch.float32, (K,)),
-            on.ptr(dX, "dX", torch.bfloat16, (M, K)), on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    i, meta = dY.get_device(), (N, K // group)
+    if not (_ok(dY, _BF, i, (M, N)) and _ok(qweight, _I32, i, (N, K // 8)) and _ok(scales, _BF, i, meta)
+            and _ok(zeros, _I32, i, meta) and _ok(dX, _BF, i, (M, K)) and _ok(workspace, _U8, i, workspace.shape)
+            and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
+        _refuse([(dY, "dY", _BF, (M, N)), (qweight, "qweight", _I32, (N, K // 8)), (scales, "scales", _BF, meta),
+                 (zeros, "zeros", _I32, meta), (dX, "dX", _BF, (M, K)), (workspace, "workspace", _U8, None)]
+                + ([(inv_s, "inv_s", _F32, (K,))] if inv_s is not None else []), i)
+    _call("w4a16_linear_dx", i, stream, dY.data_ptr(), M, N, group, qweight.data_ptr(), scales.data_ptr(),
+          zeros.data_ptr(), K, None if inv_s is None else inv_s.data_ptr(), dX.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
 
 
 def gated_backward(dH: torch.Tensor, GU: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
@@ -357,16 +375,24 @@ def gated_backward(dH: torch.Tensor, GU: torch.Tensor, qweight: torch.Tensor, sc
                    act: int = ACT_SILU, group: int = GROUP, inv_s: torch.Tensor | None = None, stream=None) -> None:
     """w4a16_gated_backward: dGU = [dH * U * act'(G) | dH * act(G)] (may be GU itself) and dX[M, K] = dGU . W_hat,
     the gradient of gated's input.  workspace: >= dx_workspace_bytes(M, N, K, group)."""
-    on = _On(dH, "dH")
     M, I = _two_dims(dH, "dH")
     N, K = qweight.shape[0], qweight.shape[1] * 8
     if N != 2 * I:
         raise ValueError("the weight must have two rows for every column of dH")
-    on.call("w4a16_gated_backward", stream, on.ptr(dH, "dH", torch.bfloat16),
-            on.ptr(GU, "GU", torch.bfloat16, (M, N)), M, N, act, group,
-            *on.weight(qweight, scales, zeros, N, K, group), K, on.opt(inv_s, "inv_s", torch.float32, (K,)),
-            on.ptr(dGU, "dGU", torch.bfloat16, (M, N)), on.ptr(dX, "dX", torch.bfloat16, (M, K)),
-            on.ptr(workspace, "workspace", torch.uint8), workspace.numel())
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    i, meta = dH.get_device(), (N, K // group)
+    if not (_ok(dH, _BF, i, (M, I)) and _ok(GU, _BF, i, (M, N)) and _ok(qweight, _I32, i, (N, K // 8))
+            and _ok(scales, _BF, i, meta) and _ok(zeros, _I32, i, meta) and _ok(dGU, _BF, i, (M, N))
+            and _ok(dX, _BF, i, (M, K)) and _ok(workspace, _U8, i, workspace.shape)
+            and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
+        _refuse([(dH, "dH", _BF, (M, I)), (GU, "GU", _BF, (M, N)), (qweight, "qweight", _I32, (N, K // 8)),
+                 (scales, "scales", _BF, meta), (zeros, "zeros", _I32, meta), (dGU, "dGU", _BF, (M, N)),
+                 (dX, "dX", _BF, (M, K)), (workspace, "workspace", _U8, None)]
+                + ([(inv_s, "inv_s", _F32, (K,))] if inv_s is not None else []), i)
+    _call("w4a16_gated_backward", i, stream, dH.data_ptr(), GU.data_ptr(), M, N, act, group, qweight.data_ptr(),
+          scales.data_ptr(), zeros.data_ptr(), K, None if inv_s is None else inv_s.data_ptr(), dGU.data_ptr(),
+          dX.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def w8_quantize(W: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, dev_status: torch.Tensor,
