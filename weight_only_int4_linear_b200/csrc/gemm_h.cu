@@ -1040,42 +1040,37 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
     }
 }
 
-// The cut tiles: adds each tile's parts in cluster order and finishes the outputs.  One block per tile and 8
-// tokens, a thread per row of the tile.
+// The cut tiles: adds each tile's parts in cluster order and finishes the outputs.  One block per tile and 4 tokens, a
+// thread per row of the tile; the loads of 4 parts are in flight together (this kernel is all latency).
+constexpr int kJoinTokens = 4, kJoinParts = 4;
 template <int MODE, int NT>
 __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
-    constexpr int T = 8;
+    constexpr int T = kJoinTokens;
     pdl_launch_dependents();
-    pdl_wait_primary();
     const int r = blockIdx.x / (NT / T), c0 = (blockIdx.x - r * (NT / T)) * T;
     int rt, mt;
     tile_coords(a.whole_tiles + r, a, rt, mt);
-    if (mt * NT + c0 >= a.M) return;
-    const int first = cta_of_unit((int64_t)r * a.NS, a.base, a.rem);
-    const int last = cta_of_unit((int64_t)r * a.NS + a.NS - 1, a.base, a.rem);
-    if (first == last) return;  // one cluster ran the tile whole
-    const int v = rt * kTileRows + threadIdx.x;
-    Extra<MODE, T> x;
-    x.load(a, mt * NT + c0, v);
-    float sum[T];
-#pragma unroll
-    for (int j = 0; j < T; ++j) sum[j] = 0.f;
     const int64_t u0 = (int64_t)r * a.NS;  // the tile's first stage
+    const int first = cta_of_unit(u0, a.base, a.rem), last = cta_of_unit(u0 + a.NS - 1, a.base, a.rem);
+    const int m0 = mt * NT + c0, v = rt * kTileRows + threadIdx.x;
+    pdl_wait_primary();
+    if (m0 >= a.M || first == last) return;  // padding, or one cluster ran the tile whole
     auto part = [&](int b) {
         const int64_t u = (int64_t)b * a.base + min(b, a.rem);  // the cluster's first stage
         return a.partial + ((int64_t)slot_of(b, u > u0 ? 1 : 0) * NT + c0) * kTileRows + threadIdx.x;
     };
-    for (int b = first; b <= last; b += 2) {  // two parts' loads in flight
-        const float *p = part(b), *q = part(min(b + 1, last));
-        float f[T], g[T];
+    float f[kJoinParts][T];
+    auto load = [&](int b0) {
 #pragma unroll
-        for (int j = 0; j < T; ++j) {
-            f[j] = __ldcg(p + j * kTileRows);
-            g[j] = b < last ? __ldcg(q + j * kTileRows) : 0.f;
+        for (int i = 0; i < kJoinParts; ++i) {
+            const float* p = part(min(b0 + i, last));
+#pragma unroll
+            for (int j = 0; j < T; ++j) f[i][j] = b0 + i <= last ? __ldcg(p + j * kTileRows) : 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < T; ++j) sum[j] = sum[j] + f[j] + g[j];
-    }
+    };
+    load(first);
+    Extra<MODE, T> x;
+    x.load(a, m0, v);
     float bias = 0.f, col_s = 1.f;
     int row_e = 0;
     if (v < a.R) {
@@ -1083,7 +1078,17 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
         if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
         if (MODE == kDx && a.inv_s) col_s = __ldg(a.inv_s + v);
     }
-    finish<MODE, T>(a, sum, x, mt * NT + c0, v, bias, row_e, col_s);
+    float sum[T];
+#pragma unroll
+    for (int j = 0; j < T; ++j) sum[j] = 0.f;
+    for (int b = first; b <= last; b += kJoinParts) {
+        if (b > first) load(b);
+#pragma unroll
+        for (int i = 0; i < kJoinParts; ++i)
+#pragma unroll
+            for (int j = 0; j < T; ++j) sum[j] += f[i][j];
+    }
+    finish<MODE, T>(a, sum, x, m0, v, bias, row_e, col_s);
 }
 
 // ------------------------------------------------------------------ host
@@ -1191,7 +1196,7 @@ int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, const CU
     cfg.gridDim = dim3((unsigned)(grid * 2));
     if (cudaLaunchKernelEx(&cfg, gemm_h_kernel<MODE, NT>, tx, tq, tm, a) != cudaSuccess) return W4A16_ERR_CUDA;
     if (cut == 0) return W4A16_OK;
-    return launch_pdl(gemm_h_join_kernel<MODE, NT>, (int64_t)cut * (NT / 8), kTileRows, stream, a);
+    return launch_pdl(gemm_h_join_kernel<MODE, NT>, (int64_t)cut * (NT / kJoinTokens), kTileRows, stream, a);
 }
 
 template <int MODE>
