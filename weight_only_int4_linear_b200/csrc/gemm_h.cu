@@ -55,31 +55,37 @@ namespace {
 
 constexpr int kBM = 128;                       // output rows per CTA
 constexpr int kTileRows = 2 * kBM;             // per cluster
-constexpr int kBK = 64;                        // contraction per stage
-constexpr int kABytes = kBM * kBK * 2;         // 16 KB
-constexpr int kCodeBytes = kBM * kBK / 2;      // 4 KB
-constexpr int kMetaBytes = 1024;               // up to 8 lines of 128 B x ... (see meta words below)
-constexpr int kDqGroups = 3;                   // groups of 4 dequantiser warps, each taking every kDqGroups-th stage
-constexpr int kDqWarps = 4 * kDqGroups, kEpiWarps = 8;  // two epilogue warps per TMEM lane quadrant
-constexpr int kTokWarp = kDqWarps + kEpiWarps;  // TMA: tokens
-constexpr int kCodeWarp = kTokWarp + 1;         // TMA: codes and meta words
-constexpr int kMmaWarp = kCodeWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kBK = 64;                        // contraction per 128-byte operand line
 constexpr int kTopExp = 15;                    // scaled operands stay below 2^15
 
 enum Mode { kLinear = 0, kGated = 1, kDx = 2 };
 
-template <int NT>
+template <int MODE, int NT>
 struct Cfg {
-    static constexpr int kXBytes = NT / 2 * kBK * 2;
-    static constexpr int kStageBytes = kXBytes + kABytes + kCodeBytes + kMetaBytes;
+    // Up to 128 tokens forward, the dequantised rows go to tensor memory (a thread's row is a TMEM lane), which leaves
+    // shared memory to codes and tokens, in stages of 128 k: with few tokens the MMAs take a third of a stage of 64
+    // (45 cycles each), and what bounds it is the fixed cost of a stage in every role.
+    static constexpr bool kTs = MODE != kDx && NT <= 128;
+    static constexpr int kHalves = kTs ? 2 : 1;         // operand lines (64 of contraction) per stage
+    static constexpr int kStageK = kHalves * kBK;
+    static constexpr int kDqGroups = kTs ? 4 : 3;       // of 4 warps
+    static constexpr int kTmaPairs = kTs ? 2 : 1;       // a warp for tokens, one for codes and meta words
+    static constexpr int kEpiWarps = kTs ? 4 : 8;       // one or two per TMEM lane quadrant
+    static constexpr int kEpiWarp = 4 * kDqGroups, kTmaWarp = kEpiWarp + kEpiWarps, kMmaWarp = kTmaWarp + 2 * kTmaPairs;
+    static constexpr int kThreads = (kMmaWarp + 1) * 32;
+    static constexpr int kXHalf = NT / 2 * kBK * 2, kXBytes = kHalves * kXHalf;
+    static constexpr int kCodeBytes = kBM * kStageK / 2;
+    static constexpr int kMetaBytes = kHalves * 1024;   // forward 128 rows x groups in the stage, backward 64 x in 128 columns
+    static constexpr int kCodeOff = kXBytes + (kTs ? 0 : kBM * kBK * 2), kMetaOff = kCodeOff + kCodeBytes;
+    static constexpr int kStageBytes = kMetaOff + kMetaBytes;
+    // Stages: a multiple of the dequantiser groups and of the TMA pairs.  A warp then comes back to a stage on every
+    // round of the ring, and the parity it waits for cannot stand for an older round (copies complete in any order).
     static constexpr int kFit = 226 * 1024 / kStageBytes;
-    // A multiple of the dequantiser groups: a group then comes back to a stage on every round of the ring, and the
-    // parity it waits for cannot stand for an older round (copies complete in any order).
-    static constexpr int kStages = (kFit < 9 ? kFit : 9) / kDqGroups * kDqGroups;
-    static_assert(kStages % kDqGroups == 0 && kStages >= kDqGroups, "stages and dequantiser groups");
-    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;  // + alignment slack
-    static constexpr uint32_t kTmemCols = 2 * NT;                          // two accumulators
+    static constexpr int kStages = (kTs || kFit < 9 ? kFit : 9) / kDqGroups * kDqGroups;
+    static constexpr int kSlots = kTs ? (512 - 2 * NT) / (kHalves * 32) : kStages;  // dequantised tiles: TMEM, or in the stage
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;           // + alignment slack
+    static constexpr uint32_t kTmemCols = kTs ? 512 : 2 * NT;                       // two accumulators, then the slots
+    static_assert(kStages % kDqGroups == 0 && kStages % kTmaPairs == 0 && kStages >= kSlots && kSlots > 1, "rings");
     static_assert(kStageBytes % 1024 == 0 && kSmem + 512 <= 232448, "shared memory per CTA");
 };
 
@@ -105,6 +111,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Pair MMA with the rows' operand in tensor memory (each CTA's own 128 rows) and the other in shared memory.
+__device__ __forceinline__ void umma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 
@@ -759,31 +775,29 @@ __device__ __forceinline__ void finish(const HArgs& a, float (&y)[T], const Extr
     }
 }
 
-// 32 values whose zero point is beyond 1024, from their 4 code words, in binary64: chunks j0 .. j0 + 3 of arow.
-__device__ __noinline__ void far_half(unsigned char* arow, const unsigned char* codes, int j0, int x, float s, int z,
-                                      int e) {
+// The 8 values of a code word whose zero point is beyond 1024, in binary64.
+__device__ __noinline__ uint4 far_word(uint32_t w, float s, int z, int e) {
     const double f = __longlong_as_double((long long)(1023 - e) << 52) * s;  // s 2^-e, |e| < 400
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[j];
-        uint32_t* out = reinterpret_cast<uint32_t*>(arow + 16 * ((j0 + j) ^ x));
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = __half_as_ushort(__double2half((double)((long long)((w >> (4 * i)) & 15u) - z) * f));
-            const uint32_t hi = __half_as_ushort(__double2half((double)((long long)((w >> (4 * i + 16)) & 15u) - z) * f));
-            out[i] = lo | (hi << 16);
-        }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = __half_as_ushort(__double2half((double)((long long)((w >> (4 * i)) & 15u) - z) * f));
+        const uint32_t hi = __half_as_ushort(__double2half((double)((long long)((w >> (4 * i + 16)) & 15u) - z) * f));
+        o[i] = lo | (hi << 16);
     }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int MODE, int NT>
-__global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_constant__ CUtensorMap tx,
+__global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1) gemm_h_kernel(const __grid_constant__ CUtensorMap tx,
                                                              const __grid_constant__ CUtensorMap tq,
                                                              const __grid_constant__ CUtensorMap tm, const HArgs a) {
-    using C = Cfg<NT>;
-    constexpr int S = C::kStages;
+    using C = Cfg<MODE, NT>;
+    constexpr int S = C::kStages, NS = C::kSlots;
     constexpr bool kBack = MODE == kDx;
     constexpr uint32_t kIdesc = idesc_f16(kTileRows, NT, kBack);
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[S], afull[S], empty[S], mdone[2], dfree[2];
+    __shared__ __align__(8) uint64_t full[S], empty[S], afull[NS], mdone[2], dfree[2];
     __shared__ __align__(8) uint64_t drained;
     __shared__ uint32_t s_tmem;
     const uint32_t raw = smem_u32(smem_raw);
@@ -796,13 +810,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 2);       // the two TMA warps
-            mbar_init(&afull[s], 4 * 2);  // one dequantiser group in each CTA
+            mbar_init(&full[s], 2);  // two TMA warps
             mbar_init(&empty[s], 1);
         }
+        for (int s = 0; s < NS; ++s) mbar_init(&afull[s], 4 * 2);  // one dequantiser group in each CTA
         for (int i = 0; i < 2; ++i) {
             mbar_init(&mdone[i], 1);
-            mbar_init(&dfree[i], kEpiWarps * 2);
+            mbar_init(&dfree[i], C::kEpiWarps * 2);
         }
         mbar_init(&drained, 1);
         fence_mbar_init();
@@ -816,19 +830,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
 
     // The issuing warps run their loops with all lanes, so that positions and descriptors stay in uniform
     // registers, and one elected lane issues: one thread's instruction latency per stage is what bounds them.
-    if (warp == kTokWarp || warp == kCodeWarp) {  // ------------------------------------------ TMA
+    if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {  // -------------------------------------- TMA
         const bool leader = elect_one();
-        const bool toks = warp == kTokWarp;
+        const bool toks = ((warp - C::kTmaWarp) & 1) == 0;
+        const int pair = (warp - C::kTmaWarp) >> 1;  // takes the ring's stages pair, pair + kTmaPairs, ...
         if (leader) {
             prefetch_tmap(toks ? &tx : &tq);
             if (!toks) prefetch_tmap(&tm);
         }
         Ring<S> r;
-        int issued = 0;
+        int passed = 0;
         bool ok = true;
         const int lg = a.group >> 6;  // log2(group / 32): 0, 1, 2
-        const int lines = kBack ? kBM / a.group : (lg == 0 ? 2 : 1);
-        const uint32_t bytes = toks ? C::kXBytes : kCodeBytes + lines * (kBack ? kBK : kBM) * 4;
+        const int lines = kBack ? kBM / a.group : max((C::kStageK / 32) >> lg, 1);  // groups in the stage
+        const uint32_t bytes = toks ? C::kXBytes : C::kCodeBytes + lines * (kBack ? kBK : kBM) * 4;
         pdl_wait_primary();  // operands and meta words come from the preparation kernels
         while (ok && seg.next(a)) {
             int rt, mt;
@@ -838,8 +853,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
             // backward: the first group of the CTA's columns (columns past K take any: they are never stored)
             const int gb = min(row0 >> (5 + lg), a.GQ - lines);
             for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
+                ++passed;
+                if (C::kTmaPairs > 1 && r.s % C::kTmaPairs != pair) continue;
                 if (!mbar_wait(&empty[r.s], r.parity ^ 1u, a.fault, 171)) {
                     ok = false;
+                    --passed;
                     break;
                 }
                 uint64_t* bar = &full[r.s];
@@ -847,34 +865,36 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
                 if (leader) {
                     mbar_arrive_expect_tx(bar, bytes);
                     if (toks) {
-                        tma_load_2d(st, &tx, ks * kBK, tok0, bar);
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+                            tma_load_2d(st + h * C::kXHalf, &tx, ks * C::kStageK + h * kBK, tok0, bar);
                     } else {
-                        unsigned char* codes = st + C::kXBytes + kABytes;
+                        unsigned char* codes = st + C::kCodeOff;
                         // codes, and one line of meta words per group: forward 128 rows, backward 64
                         if constexpr (kBack) {
                             tma_load_2d(codes, &tq, row0 / 8, ks * kBK, bar);
-                            tma_load_2d(codes + kCodeBytes, &tm, ks * kBK, gb, bar);
+                            tma_load_2d(codes + C::kCodeBytes, &tm, ks * kBK, gb, bar);
                         } else {
                             if constexpr (MODE == kGated)
-                                tma_load_3d(codes, &tq, ks * (kBK / 8), 0, row0 / 2, bar);
+                                tma_load_3d(codes, &tq, ks * (C::kStageK / 8), 0, row0 / 2, bar);
                             else
-                                tma_load_2d(codes, &tq, ks * (kBK / 8), row0, bar);
-                            tma_load_2d(codes + kCodeBytes, &tm, row0, 2 * ks >> lg, bar);
+                                tma_load_2d(codes, &tq, ks * (C::kStageK / 8), row0, bar);
+                            tma_load_2d(codes + C::kCodeBytes, &tm, row0, ks * (C::kStageK / 32) >> lg, bar);
                         }
                     }
                 }
-                ++issued;
             }
         }
-        // copies in flight land before the CTA may exit: the last S stages issued
-        for (int i = 0; i < min(issued, S); ++i) {
+        // this warp's copies in flight land before the CTA may exit: its stages among the last S
+        for (int i = 0; i < min(passed, S); ++i) {
             r.prev();
-            mbar_wait(&full[r.s], r.parity, a.fault, 172);
+            if (C::kTmaPairs == 1 || r.s % C::kTmaPairs == pair) mbar_wait(&full[r.s], r.parity, a.fault, 172);
         }
-    } else if (warp == kMmaWarp) {  // ------------------------------------------------ MMA issue
+    } else if (warp == C::kMmaWarp) {  // ------------------------------------------------ MMA issue
         if (rank == 0) {
             const bool leader = elect_one();
             Ring<S> r;
+            Ring<NS> q;  // the dequantised tiles
             int sc = 0;
             bool ok = true;
             const uint32_t x0 = smem_u32(ring), a0 = x0 + C::kXBytes;
@@ -883,9 +903,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
             while (ok && seg.next(a)) {
                 const int buf = sc & 1;
                 if (sc >= 2 && !mbar_wait(&dfree[buf], ((sc >> 1) - 1) & 1, a.fault, 173)) break;
-                for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
+                for (int ks = seg.s0; ks < seg.s1; ++ks, r.next(), q.next()) {
                     // the dequantisers of both CTAs waited on their copies first
-                    if (!mbar_wait(&afull[r.s], r.parity, a.fault, 174)) {
+                    if (!mbar_wait(&afull[q.s], q.parity, a.fault, 174)) {
                         ok = false;
                         break;
                     }
@@ -893,9 +913,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
                     const uint64_t off = (uint64_t)(r.s * (C::kStageBytes >> 4));
                     if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            umma_ss_pair(tmem + buf * NT, adesc + off + kk * kAStep, xdesc + off + kk * kXStep, kIdesc,
-                                         ks > seg.s0 || kk > 0);
+                        for (int kk = 0; kk < C::kStageK / 16; ++kk) {
+                            if constexpr (C::kTs)  // 8 columns of the tile's slot
+                                umma_ts_pair(tmem + buf * NT, tmem + 2 * NT + q.s * (C::kHalves * 32) + kk * 8,
+                                             xdesc + off + (kk >> 2) * (C::kXHalf >> 4) + (kk & 3) * kXStep, kIdesc,
+                                             ks > seg.s0 || kk > 0);
+                            else
+                                umma_ss_pair(tmem + buf * NT, adesc + off + kk * kAStep, xdesc + off + kk * kXStep, kIdesc,
+                                             ks > seg.s0 || kk > 0);
+                        }
                         umma_commit_pair(&empty[r.s], 0x3);
                     }
                 }
@@ -905,81 +931,117 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
             if (leader) umma_commit_pair(&drained, 0x1);  // every MMA issued completes before the teardown
             mbar_wait(&drained, 0, a.fault, 175);
         }
-    } else if (warp < kDqWarps) {  // ------------------------------------------------- dequantisers
-        // Group dg takes every kDqGroups-th stage, a thread 8 of its code words: forward, 64 k of output row `row`;
-        // backward, 64 columns (half h of the CTA's) of contraction step `row`.
+    } else if (warp < C::kEpiWarp) {  // ------------------------------------------------- dequantisers
+        // Group dg takes the ring's stages dg, dg + kDqGroups, ..., a thread kHalves x 8 code words of each: forward, the
+        // k of output row `row`; backward, 64 columns (half h of the CTA's) of contraction step `row`.
         const int dg = warp >> 2, tid = threadIdx.x & 127;
         const int row = kBack ? tid & 63 : tid, h = kBack ? tid >> 6 : 0;
-        // code chunks (16 bytes) of the row: forward 2, 32-byte swizzle; backward 4, this thread's 2 h and 2 h + 1,
-        // 64-byte swizzle
-        const int code0 = kBack ? row * 64 + 16 * ((2 * h) ^ ((row >> 1) & 3)) : row * 32 + 16 * ((row >> 2) & 1);
-        const int code1 = kBack ? row * 64 + 16 * ((2 * h + 1) ^ ((row >> 1) & 3)) : row * 32 + 16 * (((row >> 2) & 1) ^ 1);
-        // meta words of the thread's first and second 32 values
+        // The row's 16-byte code chunks: forward 2 or 4 in 32 or 64 bytes with the swizzle of that width, backward 4 in 64
+        // bytes, this thread's 2 h and 2 h + 1.
+        const int code_row = row * (kBack ? 64 : C::kStageK / 2);
+        const int code_x = kBack || C::kTs ? (row >> 1) & 3 : (row >> 2) & 1;
         constexpr int kLine = kBack ? kBK : kBM;
-        const int lg = a.group >> 6;  // log2(group / 32)
-        const int meta0 = ((kBack ? 2 * h >> lg : 0) * kLine + row) * 4;
-        const int meta1 = ((kBack ? 2 * h + 1 >> lg : (lg == 0 ? 1 : 0)) * kLine + row) * 4;
+        const int lg = a.group >> 6;             // log2(group / 32)
         const int a_off = h * 8192 + row * 128;  // operand row of 128 bytes, chunk j at j ^ (row % 8)
-        Ring<S> r;
-        int turn = dg;  // stages until this group's next
+        Ring<S> r, freed;  // freed: the stage whose MMAs read this tile's slot last
+        Ring<NS> slot;
+        int turn = dg, before = NS;
         bool ok = true;
         while (ok && seg.next(a)) {
             int rt, mt;
             tile_coords(seg.tile, a, rt, mt);
-            for (int ks = seg.s0; ks < seg.s1; ++ks, r.next()) {
-                if (turn-- != 0) continue;
-                turn = kDqGroups - 1;
-                const int s = r.s;
-                if (!mbar_wait(&full[s], r.parity, a.fault, 176)) {
-                    ok = false;
-                    break;
-                }
-                unsigned char* st = ring + s * C::kStageBytes;
-                unsigned char* arow = st + C::kXBytes + a_off;
-                const unsigned char* codes = st + C::kXBytes + kABytes;
-                const uint4 w0 = *reinterpret_cast<const uint4*>(codes + code0);
-                const uint4 w1 = *reinterpret_cast<const uint4*>(codes + code1);
-                const uint32_t mw[2] = {*reinterpret_cast<const uint32_t*>(codes + kCodeBytes + meta0),
-                                        *reinterpret_cast<const uint32_t*>(codes + kCodeBytes + meta1)};
-                const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            for (int ks = seg.s0; ks < seg.s1; ++ks, r.next(), slot.next()) {
+                const bool first = before > 0;  // the slots' first round
+                if (first) --before;
+                if (turn-- == 0) {
+                    turn = C::kDqGroups - 1;
+                    if (!mbar_wait(&full[r.s], r.parity, a.fault, 176) ||
+                        (C::kTs && !first && !mbar_wait(&empty[freed.s], freed.parity, a.fault, 178))) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char* st = ring + r.s * C::kStageBytes;
+                    const unsigned char* codes = st + C::kCodeOff;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t sp = __byte_perm(mw[c], mw[c], 0x1010), zp = __byte_perm(mw[c], mw[c], 0x3232);
-                    const __half2 s2 = *reinterpret_cast<const __half2*>(&sp), z2 = *reinterpret_cast<const __half2*>(&zp);
+                    for (int half = 0; half < C::kHalves; ++half) {
+                        uint32_t w[8], mw[2];
 #pragma unroll
-                    for (int j = 4 * c; j < 4 * c + 4; ++j) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t p;  // (1024 + q) of codes e and e + 4
-                            asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(p) : "r"(w[j] >> (4 * e)));
-                            const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&p), z2), s2);
-                            o[e] = *reinterpret_cast<const uint32_t*>(&v);
+                        for (int c = 0; c < 2; ++c) {  // 4 words, 32 values
+                            const int chunk = 2 * (kBack ? h : half) + c;
+                            const uint4 v = *reinterpret_cast<const uint4*>(codes + code_row + 16 * (chunk ^ code_x));
+                            w[4 * c] = v.x;
+                            w[4 * c + 1] = v.y;
+                            w[4 * c + 2] = v.z;
+                            w[4 * c + 3] = v.w;
+                            mw[c] = *reinterpret_cast<const uint32_t*>(st + C::kMetaOff + ((chunk >> lg) * kLine + row) * 4);
                         }
-                        *reinterpret_cast<uint4*>(arow + 16 * (j ^ (row & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+                        uint32_t o[32];  // the words' values, four pairs each
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t m = mw[j >> 2], sp = __byte_perm(m, m, 0x1010), zp = __byte_perm(m, m, 0x3232);
+                            const __half2 s2 = *reinterpret_cast<const __half2*>(&sp),
+                                          z2 = *reinterpret_cast<const __half2*>(&zp);
+                            const __half2 z64 = __hsub2(__float2half2_rn(960.f), z2);  // -(64 + z)
+                            // q - z of codes e and e + 4, exact: 1024 + q less 1024 + z, or (1024 + 16 q) / 16 less 64 + z
+                            const uint32_t w8 = w[j] >> 8;
+                            uint32_t p[4];
+                            asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(p[0]) : "r"(w[j]));
+                            asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(p[1]) : "r"(w[j]));
+                            asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(p[2]) : "r"(w8));
+                            asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(p[3]) : "r"(w8));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __half2 h2 = *reinterpret_cast<const __half2*>(&p[e]);
+                                const __half2 d = e & 1 ? __hfma2(h2, __float2half2_rn(0.0625f), z64) : __hsub2(h2, z2);
+                                const __half2 v = __hmul2(d, s2);
+                                o[4 * j + e] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                        }
+                        if ((mw[0] >> 16) == 0x7FFFu || (mw[1] >> 16) == 0x7FFFu) {  // rare: zero points beyond 1024
+                            const int64_t vrow =
+                                kBack ? (int64_t)ks * kBK + row : (int64_t)rt * kTileRows + rank * kBM + row;
+                            const int64_t n = MODE == kGated ? gated_row(vrow, a.I) : vrow;
+                            const int col = kBack ? rt * kTileRows + rank * kBM + h * 64 : ks * C::kStageK + half * 64;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t m = mw[j >> 2];
+                                if ((m >> 16) != 0x7FFFu) continue;
+                                const int64_t g = n * a.GQ + min((col + 32 * (j >> 2)) / a.group, a.GQ - 1);
+                                const uint4 f = far_word(w[j], bf16_bits_to_float(__ldg(a.scales + g)), __ldg(a.zeros + g),
+                                                         (int)(int16_t)(m & 0xFFFFu));
+                                o[4 * j] = f.x;
+                                o[4 * j + 1] = f.y;
+                                o[4 * j + 2] = f.z;
+                                o[4 * j + 3] = f.w;
+                            }
+                        }
+                        if constexpr (C::kTs) {
+                            __syncwarp();
+                            tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * NT + slot.s * (C::kHalves * 32) + half * 32,
+                                      o);
+                        } else {
+                            unsigned char* arow = st + C::kXBytes + a_off;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                *reinterpret_cast<uint4*>(arow + 16 * (j ^ (row & 7))) =
+                                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        }
                     }
-                }
-                if ((mw[0] >> 16) == 0x7FFFu || (mw[1] >> 16) == 0x7FFFu) {  // rare: rewrite the far half row
-                    const int64_t vrow = kBack ? (int64_t)ks * kBK + row : (int64_t)rt * kTileRows + rank * kBM + row;
-                    const int64_t n = MODE == kGated ? gated_row(vrow, a.I) : vrow;
-                    const int col = kBack ? rt * kTileRows + rank * kBM + h * 64 : ks * kBK;
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        if ((mw[c] >> 16) != 0x7FFFu) continue;
-                        const int g = min((col + 32 * c) / a.group, a.GQ - 1);
-                        far_half(arow, codes + (c ? code1 : code0), 4 * c, row & 7,
-                                 bf16_bits_to_float(__ldg(a.scales + n * a.GQ + g)), __ldg(a.zeros + n * a.GQ + g),
-                                 (int)(int16_t)(mw[c] & 0xFFFFu));
+                    if constexpr (C::kTs) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                    } else {
+                        fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor core
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(&afull[slot.s], 0);
                 }
-                fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor core
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(&afull[s], 0);
+                if (!first) freed.next();
             }
         }
     } else {  // ------------------------------------------------------------------------- epilogue
         pdl_wait_primary();  // exponents come from the preparation kernels, the residual from earlier ones
-        const int quad = warp & 3, half = (warp - kDqWarps) >> 2;
+        const int quad = warp & 3, half = (warp - C::kEpiWarp) >> 2;
         const int lrow = quad * 32 + lane;  // TMEM lane
         // backward: position (0,1,..,7) of every 8-block holds column (0,4,1,5,2,6,3,7)
         const int orow = kBack ? (lrow & ~7) | ((lrow & 7) >> 1) | ((lrow & 1) << 2) : lrow;
@@ -1005,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_h_kernel(const __grid_consta
                 if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
                 if (kBack && a.inv_s) col_s = __ldg(a.inv_s + v);
             }
-            constexpr int T = 16, kCols = NT / 2;  // this warp's columns: kCols from half * kCols
+            constexpr int T = 16, kCols = NT / (C::kEpiWarps / 4);  // this warp's columns: kCols from half * kCols
 #pragma unroll 1
             for (int cc = 0; cc < kCols; cc += T) {
                 const int c0 = half * kCols + cc, m0 = mt * NT + c0;
@@ -1142,9 +1204,10 @@ int launch_pdl(Kern kernel, int64_t grid, int block, cudaStream_t stream, Args..
 
 template <int MODE, int NT>
 int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, const CUtensorMap& tm, cudaStream_t stream) {
-    using C = Cfg<NT>;
+    using C = Cfg<MODE, NT>;
+    a.NS = (int)ceil_div(a.C, C::kStageK);
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
@@ -1184,7 +1247,7 @@ int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, const CU
     a.split_units = 0;
     if (cut > 0) {
         const int64_t stages = (int64_t)cut * a.NS;
-        int64_t parts = stages / 4;  // at least four stages each
+        int64_t parts = stages * C::kStageK / 256;  // at least four lines of 64 each
         if (parts > units) parts = units;
         if (parts < 1) parts = 1;
         a.split_units = (int)parts;
@@ -1240,21 +1303,23 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     a.GQ = (int)(K / group);
     a.group = group;
     a.N = (int)N;
-    a.NS = (int)(K / kBK);
     a.m_tiles = (int)ceil_div(M, NT);
     a.r_tiles = (int)ceil_div(N, kTileRows);
+    const uint32_t stage_k = NT == 256 ? Cfg<kLinear, 256>::kStageK : Cfg<kLinear, 64>::kStageK;
+    // a stage's codes are stage_k / 2 bytes of a row
+    const CUtensorMapSwizzle swizzle = stage_k == 64 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap tx, tq, tm;
     if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + l.op, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kBK,
                         (uint32_t)NT / 2, CU_TENSOR_MAP_SWIZZLE_128B))
         return W4A16_ERR_CUDA;
     const bool ok = e.gated ? encode_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight,
                                              {(uint64_t)K / 8, 2, (uint64_t)I}, {(uint64_t)I * K / 2, (uint64_t)K / 2},
-                                             {kBK / 8, 2, kBM / 2}, CU_TENSOR_MAP_SWIZZLE_32B)
+                                             {stage_k / 8, 2, kBM / 2}, swizzle)
                             : encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N,
-                                             (uint64_t)K / 2, kBK / 8, kBM, CU_TENSOR_MAP_SWIZZLE_32B);
-    // the meta words of a stage: its rows x the groups of its 64 k
+                                             (uint64_t)K / 2, stage_k / 8, kBM, swizzle);
+    // the meta words of a stage: 128 rows x the groups of its k
     if (!ok || !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
-                               (uint64_t)l.Rp * 4, kBM, group == 32 ? 2 : 1))
+                               (uint64_t)l.Rp * 4, kBM, stage_k > (uint32_t)group ? stage_k / (uint32_t)group : 1))
         return W4A16_ERR_CUDA;
     const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int16_t*>(ws + l.exps),
                       nullptr, (int)N, (int)l.Rp, a.GQ, I};
@@ -1291,7 +1356,6 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     a.GQ = (int)(K / group);
     a.group = group;
     a.N = (int)N;
-    a.NS = (int)ceil_div(N, kBK);
     a.m_tiles = (int)ceil_div(M, NT);
     a.r_tiles = (int)ceil_div(K, kTileRows);
     CUtensorMap tx, tq, tm;
