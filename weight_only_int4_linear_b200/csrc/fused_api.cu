@@ -21,8 +21,10 @@ bool known_act(int act) { return act >= W4A16_ACT_NONE && act <= W4A16_ACT_GELU_
 
 enum Path { kCc, kSub, kMt, kGemm };
 
-// The integer GEMVs where they exist (their conditions are those of w4a16_linear and w4a16_linear_g): at 16 tokens
-// and fewer they read the codes faster than the GEMM, whose tiles hold 64 tokens.
+// The integer GEMVs where they exist (their conditions are those of w4a16_linear and w4a16_linear_g): up to 16 tokens
+// they are ahead of the GEMM, whose tiles hold 64 tokens (5120 x 5120, 28672 x 8192, gated 5120 x 51200 and 8192 x
+// 57344, us a call with 8 tokens: 10.7 / 34.6 / 39.2 / 61.1 against 15.8 / 51 / 58 / 92; with 16 tokens 14.1 / 47.0 /
+// 55.0 / 90.1 against 15.9 / 51.1 / 57.9 / 92.5).
 Path forward_path(int64_t M, int64_t K, int group, bool scaled) {
     const bool blocks = (K / kGroup) % 8 == 0;
     if (M == 1 && group == kGroup && blocks) return kCc;
