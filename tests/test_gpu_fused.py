@@ -190,6 +190,99 @@ def test_extreme_magnitudes(cuda_lib, M):
     F.check(_linear(Z, pw), want, bound, "one-hot")
 
 
+@pytest.mark.parametrize("M", [2, 70])
+def test_gated_backward_at_the_ends_of_the_range(cuda_lib, M):
+    """Gradients of extreme size, rows of extreme weights (their powers of two are no normal FP32 numbers), and tokens
+    whose every gate is shut, whose operand is made from the rounded gradients."""
+    N, K = 514, 256
+    pw = F.make_weight(N, K, 64, seed=13, far=True)
+    pw.scales[3::7] = (pw.scales[3::7].double() * 2.0 ** -112).to(BF)
+    W = F.weight64(pw)
+    for scale in (2.0 ** 90, 2.0 ** -95, 1.0):
+        for act in (w4.ACT_SILU, w4.ACT_GELU, w4.ACT_GELU_TANH):
+            dH, GU = (_rand((M, N // 2), 1).double() * scale).to(BF), _rand((M, N), 2, 2.0)
+            shut = M // 2
+            GU[shut, : N // 2] = -abs(GU[shut, : N // 2]) - (30.0 if act == w4.ACT_SILU else 7.0)
+            d, e = F.grads64(dH, GU, act)
+            # FP32 holds the shut gates' gradients to a relative 2^-16 (a difference of two small terms, e^x for large
+            # x); below 2^-126 to half a step of its subnormals times the factors that follow
+            e[shut] = 2.0 ** -14 * (dH[shut].double().abs() * (1 + GU[shut, : N // 2].double().abs()) ** 3
+                                    * torch.exp(GU[shut, : N // 2].double())).repeat(2) * torch.cat(
+                [GU[shut, N // 2:].double().abs() + 1, torch.ones(N // 2, device="cuda", dtype=F.F8)])
+            e = e + 2.0 ** -126
+            dGU, dX = _backward(dH, GU, pw, act)
+            F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, f"dGU {scale} {act}")
+            want, bound = F.dx64(d, W, r_d=2.0 ** -8)
+            F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), f"dX {scale} {act}")
+
+
+def test_tiny_weights_both_ways(cuda_lib):
+    N, K = 260, 1024
+    pw = F.make_weight(N, K, 128, seed=14)
+    pw.scales[1::3] = (pw.scales[1::3].double() * 2.0 ** -110).to(BF)
+    W = F.weight64(pw)
+    for M in (1, 6, 40, 150):
+        X = F.tokens(M, K, 2)
+        F.check(_linear(X, pw), *F.linear64(X, W, None, w4.ACT_NONE, None), f"forward {M}")
+        dY = _rand((M, N), 3)
+        dY[:, 0::3] = 0
+        dY[:, 2::3] = 0  # only the tiny rows count
+        F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), W), f"dx {M}")
+
+
+def test_refusals_leave_the_outputs(cuda_lib):
+    N, K, M = 130, 1024, 20
+    pw = F.make_weight(N, K, 128, seed=3)
+    q = (pw.qweight, pw.scales, pw.zeros)
+    X, Y, dX = F.tokens(M, K, 1), F.nans(M, N), F.nans(M, K)
+    H, GU = F.nans(M, N // 2), F.nans(M, N)
+    ws = F.workspace(w4.fused_workspace_bytes(M, N, K))
+    short = ws[: 256 * 1024]
+
+    def status(f):
+        with pytest.raises(w4.W4A16Error) as e:
+            f()
+        return e.value.status
+
+    assert status(lambda: w4.linear_fused(X, *q, Y, short)) == w4.ERR_WORKSPACE
+    assert status(lambda: w4.gated(X, *q, H, short, GU=GU)) == w4.ERR_WORKSPACE
+    assert status(lambda: w4.linear_dx(Y, *q, dX, short)) == w4.ERR_WORKSPACE
+    assert status(lambda: w4.gated_backward(H, Y, *q, GU, dX, short)) == w4.ERR_WORKSPACE
+    assert status(lambda: w4.linear_fused(X, *q, Y, ws, act=9)) == w4.ERR_ARG
+    for bad, err in [(lambda: w4.linear_fused(X, *q, Y[:-1], ws), ValueError),
+                     (lambda: w4.linear_fused(X, *q, Y.float(), ws), TypeError),
+                     (lambda: w4.linear_fused(X.t().contiguous().t(), *q, Y, ws), ValueError),
+                     (lambda: w4.linear_fused(X, *q, Y, None), TypeError),
+                     (lambda: w4.linear_fused(X, *q, Y, ws.cpu()), ValueError),
+                     (lambda: w4.linear_fused(X, *q, Y, ws, bias=Y[0, :-1]), ValueError),
+                     (lambda: w4.linear_fused(X, *q, Y, ws, residual=X), ValueError),
+                     (lambda: w4.linear_fused(X, *q, Y, ws, group=64), ValueError),
+                     (lambda: w4.linear_fused(X, *q, Y, ws, group=96), ValueError),
+                     (lambda: w4.gated(X, *q, Y, ws), ValueError),
+                     (lambda: w4.linear_dx(X, *q, dX, ws), ValueError)]:
+        with pytest.raises(err):
+            bad()
+    _done()
+    for t in (Y, dX, H, GU):
+        assert bool(torch.isnan(t).all())
+
+
+def test_other_streams_and_raw_handles(cuda_lib):
+    N, K, M = 258, 1024, 20
+    pw = F.make_weight(N, K, 128, seed=3)
+    X, ws = F.tokens(M, K, 1), F.workspace(w4.fused_workspace_bytes(M, N, K))
+    ref = _linear(X, pw)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [F.nans(M, N) for _ in range(3)]
+    w4.linear_fused(X, pw.qweight, pw.scales, pw.zeros, outs[0], ws, stream=s)
+    w4.linear_fused(X, pw.qweight, pw.scales, pw.zeros, outs[1], ws, stream=s.cuda_stream)
+    with torch.cuda.stream(s):
+        w4.linear_fused(X, pw.qweight, pw.scales, pw.zeros, outs[2], ws)
+    _done()
+    assert all(torch.equal(ref, o) for o in outs)
+
+
 def test_rows_behind_the_last_token_stay(cuda_lib):
     N, K = 258, 1024
     pw = F.make_weight(N, K, 128, seed=2)

@@ -314,7 +314,7 @@ def linear_fused(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, z
         raise ValueError("group must be 32, 64 or 128")
     i, meta = X.get_device(), (N, K // group)
     if not (_ok(X, _BF, i, (M, K)) and _ok(qweight, _I32, i, (N, K // 8)) and _ok(scales, _BF, i, meta)
-            and _ok(zeros, _I32, i, meta) and _ok(Y, _BF, i, (M, N)) and _ok(workspace, _U8, i, workspace.shape)
+            and _ok(zeros, _I32, i, meta) and _ok(Y, _BF, i, (M, N)) and _ok(workspace, _U8, i, getattr(workspace, "shape", None))
             and (bias is None or _ok(bias, _BF, i, (N,))) and (residual is None or _ok(residual, _BF, i, (M, N)))
             and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
         _refuse([(X, "X", _BF, (M, K)), (qweight, "qweight", _I32, (N, K // 8)), (scales, "scales", _BF, meta),
@@ -339,7 +339,7 @@ def gated(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: t
         raise ValueError("group must be 32, 64 or 128")
     i, meta = X.get_device(), (N, K // group)
     if not (_ok(X, _BF, i, (M, K)) and _ok(qweight, _I32, i, (N, K // 8)) and _ok(scales, _BF, i, meta)
-            and _ok(zeros, _I32, i, meta) and _ok(H, _BF, i, (M, N // 2)) and _ok(workspace, _U8, i, workspace.shape)
+            and _ok(zeros, _I32, i, meta) and _ok(H, _BF, i, (M, N // 2)) and _ok(workspace, _U8, i, getattr(workspace, "shape", None))
             and (GU is None or _ok(GU, _BF, i, (M, N))) and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
         _refuse([(X, "X", _BF, (M, K)), (qweight, "qweight", _I32, (N, K // 8)), (scales, "scales", _BF, meta),
                  (zeros, "zeros", _I32, meta), (H, "H", _BF, (M, N // 2)), (workspace, "workspace", _U8, None)]
@@ -360,7 +360,7 @@ def linear_dx(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zer
         raise ValueError("group must be 32, 64 or 128")
     i, meta = dY.get_device(), (N, K // group)
     if not (_ok(dY, _BF, i, (M, N)) and _ok(qweight, _I32, i, (N, K // 8)) and _ok(scales, _BF, i, meta)
-            and _ok(zeros, _I32, i, meta) and _ok(dX, _BF, i, (M, K)) and _ok(workspace, _U8, i, workspace.shape)
+            and _ok(zeros, _I32, i, meta) and _ok(dX, _BF, i, (M, K)) and _ok(workspace, _U8, i, getattr(workspace, "shape", None))
             and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
         _refuse([(dY, "dY", _BF, (M, N)), (qweight, "qweight", _I32, (N, K // 8)), (scales, "scales", _BF, meta),
                  (zeros, "zeros", _I32, meta), (dX, "dX", _BF, (M, K)), (workspace, "workspace", _U8, None)]
@@ -384,7 +384,7 @@ def gated_backward(dH: torch.Tensor, GU: torch.Tensor, qweight: torch.Tensor, sc
     i, meta = dH.get_device(), (N, K // group)
     if not (_ok(dH, _BF, i, (M, I)) and _ok(GU, _BF, i, (M, N)) and _ok(qweight, _I32, i, (N, K // 8))
             and _ok(scales, _BF, i, meta) and _ok(zeros, _I32, i, meta) and _ok(dGU, _BF, i, (M, N))
-            and _ok(dX, _BF, i, (M, K)) and _ok(workspace, _U8, i, workspace.shape)
+            and _ok(dX, _BF, i, (M, K)) and _ok(workspace, _U8, i, getattr(workspace, "shape", None))
             and (inv_s is None or _ok(inv_s, _F32, i, (K,)))):
         _refuse([(dH, "dH", _BF, (M, I)), (GU, "GU", _BF, (M, N)), (qweight, "qweight", _I32, (N, K // 8)),
                  (scales, "scales", _BF, meta), (zeros, "zeros", _I32, meta), (dGU, "dGU", _BF, (M, N)),

@@ -31,7 +31,7 @@ __device__ __forceinline__ float silu_f(float x) { return x < -88.f ? x * __expf
 // Phi(x) and e^(-x^2/2): the lower tail Phi(-|x|) = e^(-x^2/2) R(t), t = 1 / (1 + 0.35 |x|), R the polynomial of degree
 // 7 with the least relative error against Phi(-|x|) e^(x^2/2) over 0 <= |x| <= 14 (3.1e-7, fitted by weighted least
 // squares; 6.2e-7 with FP32 coefficients), so the tail keeps its relative accuracy where 1 + erf would cancel.  A
-// fifth of erfcf's instructions: with it the epilogue of a 256 x 256 tile outlasted the tile's products at K = 4096.
+// fifth of erfcf's instructions, with which the epilogue of a 256 x 256 tile outlasted the tile's products at K = 4096.
 __device__ __forceinline__ float normal_cdf(float x, float& e) {
     const float t = __fdividef(1.f, fmaf(0.35f, fabsf(x), 1.f));
     e = __expf(-0.5f * x * x);

@@ -21,12 +21,13 @@
 //
 // Tile: 256 output rows (weight rows, or K columns backward) x NT tokens by a
 // cluster of two CTAs with the pair MMA (M = 256); each CTA dequantises its 128
-// rows and holds half of the tile's tokens.  Stages of 64 along the contraction.
-// Forward, a thread's 8 code words are 64 consecutive k of one row: the K-major
-// operand (K order (0,4,1,5,2,6,3,7) in every 8-block, which the token operand
-// is prepared in).  Backward, the same words are 64 consecutive output rows of
-// one contraction step: the MN-major operand, its rows in that order, which the
-// epilogue undoes in its addresses.
+// rows and holds half of the tile's tokens.
+//   * Forward, 8 code words are 64 consecutive k of one row: the K-major operand
+//     (K order (0,4,1,5,2,6,3,7) in every 8-block, which the token operand is
+//     prepared in), in shared memory, or for NT <= 128 in tensor memory.
+//   * Backward, the same words are 64 consecutive output rows of one contraction
+//     step: the MN-major operand in shared memory, its rows in that order, which
+//     the epilogue undoes in its addresses.
 //
 // Work: full waves of tiles run whole, so that the clusters sweep the same
 // operands together (L2); the last, partial wave's tiles are cut along the
@@ -37,12 +38,18 @@
 // tensor map, row 2 j + p = row p I + j, so that a pair of neighbouring lanes
 // holds both sums of an output.
 //
-// Warps: three groups of four dequantiser warps, which take the stages in turn (a
+// Warps (Cfg): groups of four dequantiser warps, which take the stages in turn (a
 // stage's dequantisation is a chain of waits -- copy, loads, stores, proxy fence --
-// longer than its MMAs), eight epilogue warps (two per TMEM lane quadrant), TMA, MMA issue
-// (rank 0).  Tokens and codes are issued by two warps: with one thread issuing every
-// copy of a stage its instruction latency, about 800 cycles, bounded the kernel.  Two accumulators: a tile's epilogue overlaps the
-// next tile's MMAs.
+// longer than its MMAs); epilogue warps, one or two per TMEM lane quadrant; TMA
+// warps for tokens and for codes and meta words (with one thread issuing every copy
+// its instruction latency, about 800 cycles a stage, bounded the kernel); one MMA
+// warp (rank 0).  Two accumulators: a tile's epilogue overlaps the next one's MMAs.
+//
+// What bounds it (1.87 GHz, MMAs of K = 16 measured at 128.5 / 65 / 45 cycles for
+// 256 / 128 / 64 tokens): with 256 tokens the MMAs, 514 of the 516-560 cycles a stage
+// of 64 takes -- 1.50 PFLOP/s on 8192 x 57344 backward and 1.55 forward, 1.60 on
+// 8192 x 10240 backward, until the power limit lowers the clock.  With few tokens the
+// dequantisers: forward 790 cycles per 128 k (2.8 TB/s of codes), backward 490 per 64.
 #include "decode_units.cuh"
 #include "epilogue.cuh"
 #include "sm100.cuh"
