@@ -65,7 +65,9 @@ def _backward(dH, GU, pw, act, inv_s=None, in_place=False):
 FORWARD = [(1, 257, 1024, 128), (1, 130, 512, 64), (1, 96, 1024, 32), (1, 77, 128, 128), (1, 300, 384, 32),
            (2, 200, 1024, 128), (9, 513, 2048, 128), (16, 129, 1024, 128), (16, 129, 640, 128), (3, 260, 512, 64),
            (17, 257, 1024, 128), (40, 1000, 384, 64), (64, 70, 256, 32), (65, 300, 1024, 128), (128, 513, 640, 128),
-           (129, 200, 2048, 64), (300, 1030, 512, 32), (513, 259, 128, 128)]
+           (129, 200, 2048, 64), (300, 1030, 512, 32), (513, 259, 128, 128),
+           # rows longer than a block's step and more than 256 groups; two waves of tiles and a rest; most of a wave
+           (20, 70, 9216, 32), (200, 130, 9216, 128), (300, 19500, 256, 128), (200, 17900, 128, 128), (90, 19500, 128, 64)]
 
 
 @pytest.mark.parametrize("M,N,K,G", FORWARD)
@@ -93,7 +95,8 @@ def test_every_activation_with_and_without_bias_and_residual(cuda_lib, M, act):
 
 @pytest.mark.parametrize("M,N,K,G", [(1, 258, 1024, 128), (1, 514, 512, 32), (1, 2, 1024, 128), (2, 402, 1024, 128),
                                      (13, 770, 2048, 128), (16, 130, 640, 64), (31, 258, 1024, 128), (64, 1026, 384, 32),
-                                     (100, 514, 512, 64), (200, 1538, 1024, 128), (260, 34, 128, 128)])
+                                     (100, 514, 512, 64), (200, 1538, 1024, 128), (260, 34, 128, 128),
+                                     (260, 19458, 128, 64), (50, 100, 9216, 32)])
 @pytest.mark.parametrize("save", [False, True])
 def test_gated_against_64_bits(cuda_lib, M, N, K, G, save):
     pw = F.make_weight(N, K, G, seed=N + K, far=True)
@@ -107,7 +110,9 @@ def test_gated_against_64_bits(cuda_lib, M, N, K, G, save):
 
 
 BACKWARD = [(1, 257, 128, 128), (1, 1000, 1024, 64), (5, 64, 384, 32), (33, 129, 640, 128), (64, 1003, 512, 64),
-            (100, 520, 1024, 32), (128, 65, 256, 128), (200, 2050, 384, 128), (300, 96, 1152, 64), (600, 770, 512, 32)]
+            (100, 520, 1024, 32), (128, 65, 256, 128), (200, 2050, 384, 128), (300, 96, 1152, 64), (600, 770, 512, 32),
+            # several steps per row of the gradients' preparation, its form for many tokens, many tiles, many groups
+            (3, 9000, 256, 128), (2, 8195, 128, 64), (601, 5000, 384, 64), (300, 130, 19456, 128), (5, 40, 9216, 32)]
 
 
 @pytest.mark.parametrize("M,N,K,G", BACKWARD)
@@ -121,7 +126,7 @@ def test_linear_dx_against_64_bits(cuda_lib, M, N, K, G):
 
 
 @pytest.mark.parametrize("M,N,K,G", [(1, 258, 128, 128), (7, 1030, 384, 64), (64, 514, 512, 32), (90, 1536, 640, 128),
-                                     (257, 130, 1024, 128), (300, 2064, 256, 32)])
+                                     (257, 130, 1024, 128), (300, 2064, 256, 32), (2, 18000, 256, 64), (3, 16402, 128, 128)])
 @pytest.mark.parametrize("act", F.ACTS)
 def test_gated_backward_against_64_bits(cuda_lib, M, N, K, G, act):
     pw = F.make_weight(N, K, G, seed=N + K + 1, far=True)
