@@ -95,9 +95,9 @@ W4A16_API int w4a16_linear_dx(const uint16_t* dY, int64_t M, int64_t N, int grou
 
 /*
  * The backward pass of w4a16_gated: dG = dH * U * act'(G) and dU = dH * act(G) from GU = [G | U], then
- * dX[m][k] = inv_s[k] * sum_j (dG[m][j] W_hat[j][k] + dU[m][j] W_hat[I + j][k]) from the unrounded dG and dU (from
- * the rounded ones for a token whose gradients are all 2^-16 or less of its largest |dH| max(2 |U|, |G|), weighted by
- * the rows' sizes: every gate that counts is shut).
+ * dX[m][k] = inv_s[k] * sum_j (dG[m][j] W_hat[j][k] + dU[m][j] W_hat[I + j][k]) from dG and dU before their rounding
+ * to BF16: as FP16 operands, off by 2^-11 of their value or 2^-39 of the token's largest |dH| max(2 |U|, |G|) weighted
+ * with the rows' sizes.  (A token whose gradients all stay 2^-24 below that -- every gate shut -- takes the BF16 ones.)
  *   dH        device, bf16 bits [M][N / 2]
  *   GU        device, bf16 bits [M][N], as w4a16_gated wrote it
  *   dGU       device, bf16 bits [M][N]: [dG | dU]   (written; may be GU itself, else must not overlap it)

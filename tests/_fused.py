@@ -116,10 +116,15 @@ def gated64(X, W, act):
     return h, eh * (1 + U16) + U16 * h.abs() + 2.0 ** -22 * h.abs() + TINY, s, e + U16 * (s.abs() + e) + TINY
 
 
-def dx64(d, W, inv_s=None, r_d: float = 0.0):
-    """d . W (d in 64 bits, its FP16 operand off by r_d relative) and the bound of the BF16 result."""
+def dx64(d, W, inv_s=None, r_d: float = 0.0, size=None):
+    """d . W (d in 64 bits, its FP16 operand off by r_d relative) and the bound of the BF16 result.
+
+    A token's operands d_n 2^e_n are scaled so that the largest -- of d, or of the bound `size` that the gated backward
+    scales by -- is in [2^14, 2^15); FP16's half step is 2^-25 at least, so each may be off by 2^-39 of it.  2^e_n |W'|
+    with |W'| < 2^15 stands for a weight row whose largest value is within 2^5 of that (2^e_n bounds the row by whole
+    powers: the exponents of scale and zero point separately): N 2^-34 of the largest |size_n| max_k |W[n][k]| in all."""
     N = W.shape[0]
-    top = (d.abs() * W.abs().amax(1)).amax(1, keepdim=True)  # a token's largest operand, for the absolute step
+    top = ((d if size is None else size).abs() * W.abs().amax(1)).amax(1, keepdim=True)
     r = 2.0 ** -11 + r_d + (N / 16 + 4) * 2.0 ** -22
     y, e = d @ W, r * (d.abs() @ W.abs()) + 2.0 ** -34 * N * top
     if inv_s is not None:
@@ -134,6 +139,13 @@ def grads64(dH, GU, act):
     # act' is a sum of terms of magnitude up to about 1.2: computed to 2^-17 absolutely
     e = torch.cat([2.0 ** -17 * (d * u).abs(), 2.0 ** -17 * (d * act64(g, act)).abs()], 1)
     return out, e
+
+
+def gated_size(dH, GU):
+    """What the gated backward scales a token by: |dH| max(2 |U|, |G|) for both halves."""
+    I = dH.shape[1]
+    b = dH.to(F8).abs() * torch.maximum(2 * GU[:, I:].to(F8).abs(), GU[:, :I].to(F8).abs())
+    return torch.cat([b, b], 1)
 
 
 def check(got: torch.Tensor, want: torch.Tensor, bound: torch.Tensor, what: str = "") -> None:

@@ -132,11 +132,12 @@ def test_gated_backward_against_64_bits(cuda_lib, M, N, K, G, act):
     pw = F.make_weight(N, K, G, seed=N + K + 1, far=True)
     dH, GU = _rand((M, N // 2), M + act, 1e-2), _rand((M, N), M + 50, 3.0)
     GU[0, :8] = torch.tensor([-100.0, 100.0, -30.0, 30.0, 0.0, -0.0, -12.0, 12.0], device="cuda", dtype=BF)
+    GU[0, 8:16] = torch.tensor([-87.0, -87.5, -88.0, -89.0, 87.5, 89.0, -3e4, 3e4], device="cuda", dtype=BF)
     d, e = F.grads64(dH, GU, act)
     dGU, dX = _backward(dH, GU, pw, act)
     F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, "dGU")
     W = F.weight64(pw)
-    want, bound = F.dx64(d, W, r_d=2.0 ** -11)
+    want, bound = F.dx64(d, W, r_d=2.0 ** -11, size=F.gated_size(dH, GU))
     F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), "dX")
     keep = GU.clone()
     dGU2, dX2 = _backward(dH, keep, pw, act, in_place=True)  # dGU in GU's place: the same bits
@@ -217,7 +218,7 @@ def test_gated_backward_at_the_ends_of_the_range(cuda_lib, M):
             e = e + 2.0 ** -126
             dGU, dX = _backward(dH, GU, pw, act)
             F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, f"dGU {scale} {act}")
-            want, bound = F.dx64(d, W, r_d=2.0 ** -8)
+            want, bound = F.dx64(d, W, r_d=2.0 ** -8, size=F.gated_size(dH, GU))
             F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), f"dX {scale} {act}")
 
 
@@ -363,7 +364,7 @@ def test_feed_forward_block_together_eager_and_captured(cuda_lib, M):
     F.check(Y, *F.linear64(H, Wd, None, w4.ACT_NONE, res), "Y")
     F.check(dH, *F.dx64(Y.to(F.F8), Wd), "dH")
     d, e = F.grads64(dH, GU, w4.ACT_SILU)
-    want, bound = F.dx64(d, Wg, r_d=2.0 ** -11)
+    want, bound = F.dx64(d, Wg, r_d=2.0 ** -11, size=F.gated_size(dH, GU))
     F.check(dX, want, bound + (1 + F.U16) * (e @ Wg.abs()), "dX")
 
     stream = torch.cuda.Stream()

@@ -19,15 +19,16 @@ struct FusedEpilogue {
     int gated;
 };
 
-// 1 / (1 + e^-x).  __expf's error grows as 2^-22 |x|, far below the 2^-9 of the BF16 store; e^-x overflowing to
-// infinity gives the limit 0.
+// 1 / (1 + e^-x), for x above kFar: past it e^-x nears 2^126, where __fdividef gives 0, and e^x itself is the value to
+// 2^-125.  __expf's error grows as 2^-22 |x|, far below the 2^-9 of the BF16 store.
+constexpr float kFar = -87.f;
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;
 
-__device__ __forceinline__ float silu_f(float x) { return x < -88.f ? x * __expf(x) : x * sigmoid_f(x); }
+__device__ __forceinline__ float silu_f(float x) { return x < kFar ? x * __expf(x) : x * sigmoid_f(x); }
 // Phi(x) and e^(-x^2/2): the lower tail Phi(-|x|) = e^(-x^2/2) R(t), t = 1 / (1 + 0.35 |x|), R the polynomial of degree
 // 7 with the least relative error against Phi(-|x|) e^(x^2/2) over 0 <= |x| <= 14 (3.1e-7, fitted by weighted least
 // squares; 6.2e-7 with FP32 coefficients), so the tail keeps its relative accuracy where 1 + erf would cancel.  A
@@ -54,7 +55,7 @@ __device__ __forceinline__ float gelu_f(float x) {
 }
 __device__ __forceinline__ float gelu_tanh_f(float x) {
     const float u = 2.f * kGeluC * (x + kGeluA * x * x * x);
-    return u < -88.f ? x * __expf(u) : x * sigmoid_f(u);
+    return u < kFar ? x * __expf(u) : x * sigmoid_f(u);
 }
 
 // x[j] = act(x[j]); the choice is uniform over the grid.
@@ -100,7 +101,7 @@ __device__ __forceinline__ void act_grads(const float (&x)[T], int act, float (&
         case W4A16_ACT_SILU:
 #pragma unroll
             for (int j = 0; j < T; ++j) {
-                const float s = x[j] < -88.f ? __expf(x[j]) : sigmoid_f(x[j]);
+                const float s = x[j] < kFar ? __expf(x[j]) : sigmoid_f(x[j]);
                 f[j] = x[j] * s;
                 d[j] = s + f[j] * (1.f - s);
             }
@@ -118,7 +119,7 @@ __device__ __forceinline__ void act_grads(const float (&x)[T], int act, float (&
 #pragma unroll
             for (int j = 0; j < T; ++j) {
                 const float x2 = x[j] * x[j], u = 2.f * kGeluC * (x[j] + kGeluA * x2 * x[j]);
-                const float s = u < -88.f ? __expf(u) : sigmoid_f(u);
+                const float s = u < kFar ? __expf(u) : sigmoid_f(u);
                 f[j] = x[j] * s;
                 // s (1 - s) vanishes long before the cubic factor overflows: past |x| = 30 it is zero in FP32
                 d[j] = fabsf(x[j]) > 30.f ? s : s + f[j] * (1.f - s) * 2.f * kGeluC * (1.f + 3.f * kGeluA * x2);

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_meta_kernel(const MetaArgs 
 //   dG = dH U act'(G),  dU = dH act(G).
 // The first pass over the row (from memory) finds an upper bound of its largest |dY 2^e| -- exact without GATED,
 // |dH| max(2 |U|, |G|) with it, which needs no activation (|act'| <= 1.13, |act(G)| <= |G|) -- and the second (from
-// L2) forms and stores the values.  Where a gated row turns out 2^-16 or more below its bound (every gate shut), its
+// L2) forms and stores the values.  Where a gated row turns out 2^-24 or more below its bound (every gate shut), its
 // operand is stored again with its true exponent, from the BF16 gradients just stored: dGU may be GU itself (a thread
 // reads its elements of GU before it writes them), which is then gone.
 // The scaling is a product by 2^e and one by 2^-a in FP32 where both and the row's bound are far from the ends of
@@ -454,9 +454,10 @@ __device__ __forceinline__ int exp_of(float x) {
     const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
     return u == 0 ? kNothing : max((int)(u >> 23), 1) - 127;
 }
-// Bits a gated row may stay under its bound before it is stored again: FP16 has 29 binades of full precision, so that
-// 16 leave the row's largest 13, and steps of 2^-24 of its largest value below them.
-constexpr int kFarBelow = 16;
+// Bits a gated row may stay under its bound before it is stored again.  The bound is scaled to 2^14 .. 2^15 and FP16's
+// half step is 2^-25 below 2^-14, so a row 24 bits under it is still off by at most 2^-15 of its largest value, where
+// the BF16 gradients are off by 2^-8 of each.
+constexpr int kFarBelow = 24;
 
 template <bool VEC, bool GATED, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs g) {
