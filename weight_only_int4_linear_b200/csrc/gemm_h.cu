@@ -93,7 +93,7 @@ struct Cfg {
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;           // + alignment slack
     static constexpr uint32_t kTmemCols = kTs ? 512 : 2 * NT;                       // two accumulators, then the slots
     static_assert(kStages % kDqGroups == 0 && kStages % kTmaPairs == 0 && kStages >= kSlots && kSlots > 1, "rings");
-    static_assert(kStageBytes % 1024 == 0 && kSmem + 512 <= 232448, "shared memory per CTA");
+    static_assert(kStageBytes % 1024 == 0 && kSmem + 512 + 2 * NT * 4 <= 232448, "shared memory per CTA");
 };
 
 // Instruction descriptor, kind::f16 with FP16 A and B and an FP32 accumulator; A MN-major for the backward.
@@ -715,62 +715,84 @@ struct Ring {
 // starts inside a tile (its first) and one that starts a tile and does not end it (its last).
 __device__ __forceinline__ int slot_of(int b, int s0) { return 2 * b + (s0 == 0 ? 1 : 0); }
 
-// What T tokens of an output row need beside their sums, loaded ahead of them: the tokens' exponents (m0 a multiple
-// of 4; texp has room for whole tiles) and the residual.
+// The residual of T tokens of output row v from token m0 (zero where there is none), loaded ahead of the sums.
 template <int MODE, int T>
-struct Extra {
-    int te[T];
-    uint16_t res[MODE == kLinear ? T : 1];
-    __device__ __forceinline__ void load(const HArgs& a, int m0, int v) {
+__device__ __forceinline__ void load_residual(const HArgs& a, int m0, int v, uint16_t (&res)[MODE == kLinear ? T : 1]) {
+    if constexpr (MODE == kLinear) {
+        const uint16_t* r = a.ep.residual + (int64_t)m0 * a.R + v;
+        const bool ok = a.ep.residual && v < a.R;
 #pragma unroll
-        for (int j = 0; j < T; j += 4) {
-            const int4 t = __ldcg(reinterpret_cast<const int4*>(a.texp + m0 + j));
-            te[j] = t.x;
-            te[j + 1] = t.y;
-            te[j + 2] = t.z;
-            te[j + 3] = t.w;
-        }
-        if constexpr (MODE == kLinear) {
-            const uint16_t* r = a.ep.residual + (int64_t)m0 * a.R + v;
+        for (int j = 0; j < T; ++j, r += a.R) res[j] = ok && m0 + j < a.M ? __ldcg(r) : (uint16_t)0;
+    }
+}
+// T tokens' exponents, te 16-byte aligned.
+template <int T>
+__device__ __forceinline__ void load_te(const int* te, int (&e)[T]) {
 #pragma unroll
-            for (int j = 0; j < T; ++j)
-                res[j] = a.ep.residual && v < a.R && m0 + j < a.M ? __ldcg(r + (int64_t)j * a.R) : (uint16_t)0;
+    for (int j = 0; j < T; j += 4) {
+        const int4 t = *reinterpret_cast<const int4*>(te + j);
+        e[j] = t.x;
+        e[j + 1] = t.y;
+        e[j + 2] = t.z;
+        e[j + 3] = t.w;
+    }
+}
+
+// What an output row brings to all of its tokens.
+struct RowValues {
+    float bias, col_s;
+    int e;
+    template <int MODE>
+    __device__ __forceinline__ void load(const HArgs& a, int v) {
+        bias = 0.f;
+        col_s = 1.f;
+        e = 0;
+        if (v < a.R) {
+            if (MODE != kDx) e = __ldcg(a.exps + v);
+            if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
+            if (MODE == kDx && a.inv_s) col_s = __ldg(a.inv_s + v);
         }
     }
 };
 
-// Finishes T tokens of one output row: y[j] (the raw sum) belongs to token m0 + j and output row v.  All lanes of a
-// warp call it together, with consecutive v from an even one (gated rows are exchanged between neighbours).
+// Finishes T tokens of one output row: y[j] (the raw sum) belongs to token m0 + j, of exponent te[j], and output row v.
+// All lanes of a warp call it together, with consecutive v from an even one (gated rows are exchanged between
+// neighbours).  near: no token brings the row's exponent to the ends of FP32's range, one product scales a sum.
 template <int MODE, int T>
-__device__ __forceinline__ void finish(const HArgs& a, float (&y)[T], const Extra<MODE, T>& x, int m0, int v,
-                                       float bias, int row_e, float col_s) {
+__device__ __forceinline__ void finish(const HArgs& a, float (&y)[T], const int (&te)[T],
+                                       const uint16_t (&res)[MODE == kLinear ? T : 1], int m0, int v,
+                                       const RowValues& r, bool near) {
     const bool row_ok = v < a.R;
+    if (near) {
 #pragma unroll
-    for (int j = 0; j < T; ++j) y[j] = scale2(y[j], row_e + x.te[j]);
+        for (int j = 0; j < T; ++j) y[j] *= __uint_as_float((uint32_t)(r.e + te[j] + 127) << 23);
+    } else {
+#pragma unroll
+        for (int j = 0; j < T; ++j) y[j] = scale2(y[j], r.e + te[j]);
+    }
+    // out[j stride] = f[j] for the tokens m + j that exist
+    auto store = [&](uint16_t* out, int64_t stride, int m, const auto& f) {
+        constexpr int n = sizeof(f) / sizeof(float);
+#pragma unroll
+        for (int j = 0; j < n; ++j, out += stride)
+            if (row_ok && m + j < a.M) *out = to_bf16(f[j]);
+    };
     if constexpr (MODE != kGated) {
         if constexpr (MODE == kDx) {
 #pragma unroll
-            for (int j = 0; j < T; ++j) y[j] *= col_s;
+            for (int j = 0; j < T; ++j) y[j] *= r.col_s;
         } else {
 #pragma unroll
-            for (int j = 0; j < T; ++j) y[j] += bias;
+            for (int j = 0; j < T; ++j) y[j] += r.bias;
             act_all<T>(y, a.ep.act);
 #pragma unroll
-            for (int j = 0; j < T; ++j) y[j] += bf16_bits_to_float(x.res[j]);
+            for (int j = 0; j < T; ++j) y[j] += bf16_bits_to_float(res[j]);
         }
-        uint16_t* out = a.Y + (int64_t)m0 * a.R + v;
-#pragma unroll
-        for (int j = 0; j < T; ++j)
-            if (row_ok && m0 + j < a.M) out[(int64_t)j * a.R] = to_bf16(y[j]);
+        store(a.Y + (int64_t)m0 * a.R + v, a.R, m0, y);
     } else {
         const int p = v & 1;
         const int64_t col = v >> 1;
-        if (a.ep.GU) {
-            uint16_t* out = a.ep.GU + (int64_t)m0 * 2 * a.I + p * a.I + col;
-#pragma unroll
-            for (int j = 0; j < T; ++j)
-                if (row_ok && m0 + j < a.M) out[(int64_t)j * 2 * a.I] = to_bf16(y[j]);
-        }
+        if (a.ep.GU) store(a.ep.GU + (int64_t)m0 * 2 * a.I + p * a.I + col, 2 * a.I, m0, y);
         // the even lane finishes the first half of the tokens, the odd lane the second
         float gate[T / 2], up[T / 2];
 #pragma unroll
@@ -780,11 +802,10 @@ __device__ __forceinline__ void finish(const HArgs& a, float (&y)[T], const Extr
             up[j] = p ? y[T / 2 + j] : got;
         }
         act_all<T / 2>(gate, a.ep.act);
-        const int m = m0 + (p ? T / 2 : 0);
-        uint16_t* out = a.Y + (int64_t)m * a.I + col;
 #pragma unroll
-        for (int j = 0; j < T / 2; ++j)
-            if (row_ok && m + j < a.M) out[(int64_t)j * a.I] = to_bf16(gate[j] * up[j]);
+        for (int j = 0; j < T / 2; ++j) gate[j] *= up[j];
+        const int m = m0 + (p ? T / 2 : 0);
+        store(a.Y + (int64_t)m * a.I + col, a.I, m, gate);
     }
 }
 
@@ -813,6 +834,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1) gemm_h_kernel(cons
     __shared__ __align__(8) uint64_t full[S], empty[S], afull[NS], mdone[2], dfree[2];
     __shared__ __align__(8) uint64_t drained;
     __shared__ uint32_t s_tmem;
+    __shared__ __align__(16) int s_te[2][NT];  // the tokens' exponents of the tile in each accumulator
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // same offset in both CTAs
 
@@ -1065,43 +1087,67 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1) gemm_h_kernel(cons
             int rt, mt;
             tile_coords(seg.tile, a, rt, mt);
             const int buf = sc & 1;
+            const bool whole = seg.s0 == 0 && seg.s1 == a.NS;
+            const int trow = rank * kBM + orow, v = rt * kTileRows + trow;
+            constexpr int T = 8, kCols = NT / (C::kEpiWarps / 4);  // this warp's columns: kCols from half * kCols
+            const int c0 = half * kCols, m0 = mt * NT + c0;
+            // While the tile is multiplied: the row's values, the first residuals, and the tokens' exponents in shared
+            // memory with whether they keep every sum's scale inside FP32's range.  (Loaded with each batch instead, their
+            // latency made the epilogue as long as a tile of K = 4096.)
+            RowValues rv;
+            rv.load<MODE>(a, v);
+            uint16_t res[MODE == kLinear ? T : 1] = {};
+            bool near = false;
+            if (whole) {
+                load_residual<MODE, T>(a, m0, v, res);
+                for (int i = threadIdx.x - C::kEpiWarp * 32; i < NT; i += C::kEpiWarps * 32)
+                    s_te[buf][i] = mt * NT + i < a.M ? __ldcg(a.texp + mt * NT + i) : 0;
+            }
+            named_barrier_sync(1, C::kEpiWarps * 32);  // also: every warp is done with the exponents of two segments ago
+            if (whole) {
+                int lo = 0, hi = 0;
+                for (int i = lane; i < NT; i += 32) {
+                    lo = min(lo, s_te[buf][i]);
+                    hi = max(hi, s_te[buf][i]);
+                }
+                lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+                hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+                near = __all_sync(0xFFFFFFFFu, rv.e + lo >= -126 && rv.e + hi <= 127);
+            }
             if (ok && !mbar_wait(&mdone[buf], (sc >> 1) & 1, a.fault, 177)) ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);
             ++sc;
             if (!ok) continue;
             tc_fence_after();
-            const bool whole = seg.s0 == 0 && seg.s1 == a.NS;
-            const int trow = rank * kBM + orow, v = rt * kTileRows + trow;
-            float* part = a.partial + (int64_t)slot_of(b, seg.s0) * NT * kTileRows + trow;
-            float bias = 0.f, col_s = 1.f;
-            int row_e = 0;
-            if (v < a.R) {
-                if constexpr (!kBack) row_e = __ldcg(a.exps + v);
-                if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
-                if (kBack && a.inv_s) col_s = __ldg(a.inv_s + v);
-            }
-            constexpr int T = 16, kCols = NT / (C::kEpiWarps / 4);  // this warp's columns: kCols from half * kCols
+            float* part = a.partial + ((int64_t)slot_of(b, seg.s0) * NT + c0) * kTileRows + trow;
+            uint32_t d[T];
+            tmem_ld8(tl + buf * NT + c0, d);
 #pragma unroll 1
-            for (int cc = 0; cc < kCols; cc += T) {
-                const int c0 = half * kCols + cc, m0 = mt * NT + c0;
-                Extra<MODE, T> x;
-                if (whole && m0 < a.M) x.load(a, m0, v);
-                uint32_t d[T];
-                tmem_ld16(tl + buf * NT + c0, d);
+            for (int cc = 0; cc < kCols; cc += T, part += T * kTileRows) {
                 tmem_wait_ld();
-                if (cc + T == kCols) {
+                float y[T];
+                uint16_t rc[MODE == kLinear ? T : 1];
+#pragma unroll
+                for (int j = 0; j < T; ++j) y[j] = __uint_as_float(d[j]);
+#pragma unroll
+                for (int j = 0; j < (MODE == kLinear ? T : 1); ++j) rc[j] = res[j];
+                if (cc + T < kCols) {  // the next batch's loads
+                    tmem_ld8(tl + buf * NT + c0 + cc + T, d);
+                    if (whole) load_residual<MODE, T>(a, m0 + cc + T, v, res);
+                } else {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(&dfree[buf], 0);
                 }
                 if (whole) {
-                    float sum[T];
-#pragma unroll
-                    for (int j = 0; j < T; ++j) sum[j] = __uint_as_float(d[j]);
-                    if (m0 < a.M) finish<MODE, T>(a, sum, x, m0, v, bias, row_e, col_s);
+                    if (m0 + cc < a.M) {
+                        int te[T];
+                        load_te<T>(&s_te[buf][c0 + cc], te);
+                        finish<MODE, T>(a, y, te, rc, m0 + cc, v, rv, near);
+                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < T; ++j) part[(int64_t)(c0 + j) * kTileRows] = __uint_as_float(d[j]);
+                    for (int j = 0; j < T; ++j) part[j * kTileRows] = y[j];
                 }
             }
         }
@@ -1144,15 +1190,12 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
         }
     };
     load(first);
-    Extra<MODE, T> x;
-    x.load(a, m0, v);
-    float bias = 0.f, col_s = 1.f;
-    int row_e = 0;
-    if (v < a.R) {
-        if (MODE != kDx) row_e = __ldcg(a.exps + v);
-        if (MODE == kLinear && a.ep.bias) bias = load_bf16(a.ep.bias + v);
-        if (MODE == kDx && a.inv_s) col_s = __ldg(a.inv_s + v);
-    }
+    uint16_t res[MODE == kLinear ? T : 1];
+    load_residual<MODE, T>(a, m0, v, res);
+    const int4 t4 = __ldcg(reinterpret_cast<const int4*>(a.texp + m0));
+    const int te[T] = {t4.x, t4.y, t4.z, t4.w};
+    RowValues rv;
+    rv.load<MODE>(a, v);
     float sum[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) sum[j] = 0.f;
@@ -1163,7 +1206,7 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
 #pragma unroll
             for (int j = 0; j < T; ++j) sum[j] += f[i][j];
     }
-    finish<MODE, T>(a, sum, x, m0, v, bias, row_e, col_s);
+    finish<MODE, T>(a, sum, te, res, m0, v, rv, false);
 }
 
 // ------------------------------------------------------------------ host
