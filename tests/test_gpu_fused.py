@@ -222,6 +222,30 @@ def test_gated_backward_at_the_ends_of_the_range(cuda_lib, M):
             F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), f"dX {scale} {act}")
 
 
+@pytest.mark.parametrize("M", [20, 90, 300])
+def test_whole_tiles_of_tokens_and_rows_of_every_size(cuda_lib, M):
+    """A wave of uncut tiles whose tokens, and whose rows, span FP32's range, beside tiles of ordinary ones."""
+    n = 19500  # 77 tiles of rows, more than a wave of the 74 clusters for every tile width
+    size = torch.ones(M, 1, dtype=F.F8, device="cuda")
+    size[1::5], size[3::5] = 2.0 ** 100, 2.0 ** -100
+    pw = F.make_weight(n, 128, 64, seed=21)
+    pw.scales[300:800:3] = (pw.scales[300:800:3].double() * 2.0 ** -110).to(BF)
+    W = F.weight64(pw)
+    X = (F.tokens(M, 128, 4).double() * size).to(BF)
+    bias, residual = _rand((n,), 5), _rand((M, n), 6)
+    F.check(_linear(X, pw, bias, w4.ACT_RELU, residual), *F.linear64(X, W, bias, w4.ACT_RELU, residual), "linear")
+    F.check(_linear(X, pw), *F.linear64(X, W, None, w4.ACT_NONE, None), "plain")
+    small = X.clone()
+    small[1::5] = F.tokens(M, 128, 4)[1::5]  # a product of two halves of 2^100 is past BF16
+    want, bound, gu, gu_bound = F.gated64(small, W, w4.ACT_RELU)
+    H, GU = _gated(small, pw, w4.ACT_RELU, True)
+    F.check(GU, gu, gu_bound, "GU")
+    F.check(H, want, bound, "H")
+    pw = F.make_weight(130, 19456, 128, seed=22)
+    dY = (_rand((M, 130), 8).double() * size).to(BF)
+    F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), F.weight64(pw)), "dx")
+
+
 def test_tiny_weights_both_ways(cuda_lib):
     N, K = 260, 1024
     pw = F.make_weight(N, K, 128, seed=14)
