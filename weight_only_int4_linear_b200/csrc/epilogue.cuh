@@ -28,37 +28,90 @@ constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;
 
-__device__ __forceinline__ float silu_f(float x) { return x < kFar ? x * __expf(x) : x * sigmoid_f(x); }
 // Phi(x) and e^(-x^2/2): the lower tail Phi(-|x|) = e^(-x^2/2) R(t), t = 1 / (1 + 0.35 |x|), R the polynomial of degree
 // 7 with the least relative error against Phi(-|x|) e^(x^2/2) over 0 <= |x| <= 14 (3.1e-7, fitted by weighted least
 // squares; 6.2e-7 with FP32 coefficients), so the tail keeps its relative accuracy where 1 + erf would cancel.  A
 // fifth of erfcf's instructions, with which the epilogue of a 256 x 256 tile outlasted the tile's products at K = 4096.
+__device__ constexpr float kTail[8] = {-2.7316276828059927e-05f, 0.14027035236358643f, 0.13335497677326202f,
+                                       0.15596191585063934f,     -0.0170243252068758f, 0.24064184725284576f,
+                                       -0.20211991667747498f,    0.048942599445581436f};
 __device__ __forceinline__ float normal_cdf(float x, float& e) {
     const float t = __fdividef(1.f, fmaf(0.35f, fabsf(x), 1.f));
     e = __expf(-0.5f * x * x);
-    float r = 0.048942599445581436f;
-    r = fmaf(r, t, -0.20211991667747498f);
-    r = fmaf(r, t, 0.24064184725284576f);
-    r = fmaf(r, t, -0.0170243252068758f);
-    r = fmaf(r, t, 0.15596191585063934f);
-    r = fmaf(r, t, 0.13335497677326202f);
-    r = fmaf(r, t, 0.14027035236358643f);
-    r = fmaf(r, t, -2.7316276828059927e-05f);
+    float r = kTail[7];
+#pragma unroll
+    for (int i = 6; i >= 0; --i) r = fmaf(r, t, kTail[i]);
     const float h = e * r;
     return x < 0.f ? h : 1.f - h;
 }
-// GELU by the normal distribution and by a sigmoid (0.5 (1 + tanh u) = sigmoid(2 u)): neither form cancels for
-// negative x.
-__device__ __forceinline__ float gelu_f(float x) {
-    float e;
-    return x * normal_cdf(x, e);
+// Two FP32 values in one 64-bit register, for the packed instructions (half the issue slots of the epilogues).
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
 }
-__device__ __forceinline__ float gelu_tanh_f(float x) {
-    const float u = 2.f * kGeluC * (x + kGeluA * x * x * x);
-    return u < kFar ? x * __expf(u) : x * sigmoid_f(u);
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ float ex2_f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// x[j] = act(x[j]); the choice is uniform over the grid.
+// The activations of a pair, with one exponential e^-|u| each.  It is taken 2^16 times larger, so that it flushes to
+// zero only where the result is below half of BF16's smallest step; adding 16 to its exponent costs 2^-20.5 of it.
+//   x sigmoid(u), u of x's sign, t = e^-|u|:  (max(x, 0) + min(x, 0) t) / (1 + t)      (SILU: u = x)
+//   x Phi(x), tail h = Phi(-|x|):             max(x, 0) - |x| h                        (zero from |x| = 16 on)
+// None cancels for negative x.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ uint64_t x_sigmoid2(float x, float y, float u, float v) {
+    const uint64_t t = pack2(ex2_f(fmaf(-fabsf(u), kLog2e, 16.f)), ex2_f(fmaf(-fabsf(v), kLog2e, 16.f)));
+    const uint64_t down = pack2(0x1p-16f, 0x1p-16f);
+    float d, e;
+    unpack2(fma2(t, down, pack2(1.f, 1.f)), d, e);
+    const uint64_t n = fma2(mul2(pack2(fminf(x, 0.f), fminf(y, 0.f)), t), down, pack2(fmaxf(x, 0.f), fmaxf(y, 0.f)));
+    return mul2(n, pack2(rcp_f(d), rcp_f(e)));
+}
+__device__ __forceinline__ void silu2(float& x, float& y) { unpack2(x_sigmoid2(x, y, x, y), x, y); }
+__device__ __forceinline__ void gelu_tanh2(float& x, float& y) {  // 0.5 (1 + tanh u) = sigmoid(2 u)
+    const uint64_t p = pack2(x, y);
+    float u, v;
+    unpack2(mul2(fma2(mul2(p, p), pack2(2.f * kGeluC * kGeluA, 2.f * kGeluC * kGeluA), pack2(2.f * kGeluC, 2.f * kGeluC)), p),
+            u, v);
+    unpack2(x_sigmoid2(x, y, u, v), x, y);
+}
+__device__ __forceinline__ void gelu2(float& x, float& y) {
+    const float ax = fminf(fabsf(x), 16.f), ay = fminf(fabsf(y), 16.f);
+    const uint64_t t = pack2(rcp_f(fmaf(0.35f, ax, 1.f)), rcp_f(fmaf(0.35f, ay, 1.f)));
+    const uint64_t q = pack2(ax, ay);
+    float d, e;
+    unpack2(fma2(mul2(q, q), pack2(-0.5f * kLog2e, -0.5f * kLog2e), pack2(16.f, 16.f)), d, e);
+    uint64_t r = pack2(kTail[7] * 0x1p-16f, kTail[7] * 0x1p-16f);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) r = fma2(r, t, pack2(kTail[i] * 0x1p-16f, kTail[i] * 0x1p-16f));
+    float g, h;
+    unpack2(mul2(pack2(ex2_f(d), ex2_f(e)), r), g, h);
+    x = fmaf(-ax, g, fmaxf(x, 0.f));
+    y = fmaf(-ay, h, fmaxf(y, 0.f));
+}
+
+// x[j] = act(x[j]), T even; the choice is uniform over the grid.
 template <int T>
 __device__ __forceinline__ void act_all(float (&x)[T], int act) {
     switch (act) {
@@ -68,22 +121,22 @@ __device__ __forceinline__ void act_all(float (&x)[T], int act) {
             break;
         case W4A16_ACT_SILU:
 #pragma unroll
-            for (int j = 0; j < T; ++j) x[j] = silu_f(x[j]);
+            for (int j = 0; j < T; j += 2) silu2(x[j], x[j + 1]);
             break;
         case W4A16_ACT_GELU:
 #pragma unroll
-            for (int j = 0; j < T; ++j) x[j] = gelu_f(x[j]);
+            for (int j = 0; j < T; j += 2) gelu2(x[j], x[j + 1]);
             break;
         case W4A16_ACT_GELU_TANH:
 #pragma unroll
-            for (int j = 0; j < T; ++j) x[j] = gelu_tanh_f(x[j]);
+            for (int j = 0; j < T; j += 2) gelu_tanh2(x[j], x[j + 1]);
             break;
         default: break;
     }
 }
 __device__ __forceinline__ float act_f(float x, int act) {
-    float v[1] = {x};
-    act_all<1>(v, act);
+    float v[2] = {x, x};
+    act_all<2>(v, act);
     return v[0];
 }
 

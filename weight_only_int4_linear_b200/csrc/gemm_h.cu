@@ -725,9 +725,13 @@ __device__ __forceinline__ void load_residual(const HArgs& a, int m0, int v, uin
         for (int j = 0; j < T; ++j, r += a.R) res[j] = ok && m0 + j < a.M ? __ldcg(r) : (uint16_t)0;
     }
 }
-// T tokens' exponents, te 16-byte aligned.
+// A token's exponent a as the bits of 2^a where |a| <= kNear, else as a itself.
+constexpr int kNear = 60, kNearBits = (127 - kNear) << 23;
+__device__ __forceinline__ int scale_bits(int a) { return a >= -kNear && a <= kNear ? (a + 127) << 23 : a; }
+__device__ __forceinline__ int scale_exp(int bits) { return bits >= kNearBits ? (bits >> 23) - 127 : bits; }
+// T tokens' scales, 16-byte aligned.
 template <int T>
-__device__ __forceinline__ void load_te(const int* te, int (&e)[T]) {
+__device__ __forceinline__ void load_scales(const int* te, int (&e)[T]) {
 #pragma unroll
     for (int j = 0; j < T; j += 4) {
         const int4 t = *reinterpret_cast<const int4*>(te + j);
@@ -755,44 +759,58 @@ struct RowValues {
     }
 };
 
-// Finishes T tokens of one output row: y[j] (the raw sum) belongs to token m0 + j, of exponent te[j], and output row v.
+// Finishes T tokens of one output row: y[j] (the raw sum) belongs to token m0 + j, of scale bits te[j], and output row v.
 // All lanes of a warp call it together, with consecutive v from an even one (gated rows are exchanged between
-// neighbours).  near: no token brings the row's exponent to the ends of FP32's range, one product scales a sum.
+// neighbours).  near: every token's and every row's exponent is within kNear of zero, so that no partial product of the
+// scaling leaves FP32's normal range (sums are multiples of 2^-48 below 2^62).
 template <int MODE, int T>
 __device__ __forceinline__ void finish(const HArgs& a, float (&y)[T], const int (&te)[T],
                                        const uint16_t (&res)[MODE == kLinear ? T : 1], int m0, int v,
                                        const RowValues& r, bool near) {
     const bool row_ok = v < a.R;
-    if (near) {
+    if (near) {  // scale, then row factor and bias, two tokens an instruction
+        const float f = MODE == kDx ? r.col_s : __int_as_float(scale_bits(r.e));
+        const uint64_t f2 = pack2(f, f), b2 = pack2(r.bias, r.bias);
 #pragma unroll
-        for (int j = 0; j < T; ++j) y[j] *= __uint_as_float((uint32_t)(r.e + te[j] + 127) << 23);
+        for (int j = 0; j < T; j += 2) {
+            const uint64_t s = mul2(pack2(y[j], y[j + 1]), pack2(__int_as_float(te[j]), __int_as_float(te[j + 1])));
+            unpack2(MODE == kLinear ? fma2(s, f2, b2) : mul2(s, f2), y[j], y[j + 1]);
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < T; ++j) y[j] = scale2(y[j], r.e + te[j]);
+        for (int j = 0; j < T; ++j) {
+            y[j] = scale2(y[j], r.e + scale_exp(te[j]));
+            if (MODE == kDx) y[j] *= r.col_s;
+            if (MODE == kLinear) y[j] += r.bias;
+        }
     }
     // out[j stride] = f[j] for the tokens m + j that exist
-    auto store = [&](uint16_t* out, int64_t stride, int m, const auto& f) {
+    auto store = [&](uint16_t* out, int stride, int m, const auto& f) {
         constexpr int n = sizeof(f) / sizeof(float);
+        if (!row_ok) return;
+        uint32_t w[n / 2];
+#pragma unroll
+        for (int j = 0; j < n; j += 2) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[j], f[j + 1]);
+            w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
 #pragma unroll
         for (int j = 0; j < n; ++j, out += stride)
-            if (row_ok && m + j < a.M) *out = to_bf16(f[j]);
+            if (m + j < a.M) *out = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
     };
     if constexpr (MODE != kGated) {
-        if constexpr (MODE == kDx) {
-#pragma unroll
-            for (int j = 0; j < T; ++j) y[j] *= r.col_s;
-        } else {
-#pragma unroll
-            for (int j = 0; j < T; ++j) y[j] += r.bias;
+        if constexpr (MODE == kLinear) {
             act_all<T>(y, a.ep.act);
+            if (a.ep.residual) {
 #pragma unroll
-            for (int j = 0; j < T; ++j) y[j] += bf16_bits_to_float(res[j]);
+                for (int j = 0; j < T; ++j) y[j] += bf16_bits_to_float(res[j]);
+            }
         }
         store(a.Y + (int64_t)m0 * a.R + v, a.R, m0, y);
     } else {
         const int p = v & 1;
         const int64_t col = v >> 1;
-        if (a.ep.GU) store(a.ep.GU + (int64_t)m0 * 2 * a.I + p * a.I + col, 2 * a.I, m0, y);
+        if (a.ep.GU) store(a.ep.GU + (int64_t)m0 * a.R + p * (int64_t)a.I + col, a.R, m0, y);
         // the even lane finishes the first half of the tokens, the odd lane the second
         float gate[T / 2], up[T / 2];
 #pragma unroll
@@ -1102,18 +1120,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1) gemm_h_kernel(cons
             if (whole) {
                 load_residual<MODE, T>(a, m0, v, res);
                 for (int i = threadIdx.x - C::kEpiWarp * 32; i < NT; i += C::kEpiWarps * 32)
-                    s_te[buf][i] = mt * NT + i < a.M ? __ldcg(a.texp + mt * NT + i) : 0;
+                    s_te[buf][i] = scale_bits(mt * NT + i < a.M ? __ldcg(a.texp + mt * NT + i) : 0);
             }
             named_barrier_sync(1, C::kEpiWarps * 32);  // also: every warp is done with the exponents of two segments ago
             if (whole) {
-                int lo = 0, hi = 0;
-                for (int i = lane; i < NT; i += 32) {
-                    lo = min(lo, s_te[buf][i]);
-                    hi = max(hi, s_te[buf][i]);
-                }
-                lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-                hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-                near = __all_sync(0xFFFFFFFFu, rv.e + lo >= -126 && rv.e + hi <= 127);
+                near = rv.e >= -kNear && rv.e <= kNear;
+                for (int i = lane; i < NT; i += 32)
+                    near = near && s_te[buf][i] >= kNearBits;
+                near = __all_sync(0xFFFFFFFFu, near);
             }
             if (ok && !mbar_wait(&mdone[buf], (sc >> 1) & 1, a.fault, 177)) ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1143,7 +1157,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1) gemm_h_kernel(cons
                 if (whole) {
                     if (m0 + cc < a.M) {
                         int te[T];
-                        load_te<T>(&s_te[buf][c0 + cc], te);
+                        load_scales<T>(&s_te[buf][c0 + cc], te);
                         finish<MODE, T>(a, y, te, rc, m0 + cc, v, rv, near);
                     }
                 } else {
@@ -1194,7 +1208,7 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
     uint16_t res[MODE == kLinear ? T : 1];
     load_residual<MODE, T>(a, m0, v, res);
     const int4 t4 = __ldcg(reinterpret_cast<const int4*>(a.texp + m0));
-    const int te[T] = {t4.x, t4.y, t4.z, t4.w};
+    const int te[T] = {scale_bits(t4.x), scale_bits(t4.y), scale_bits(t4.z), scale_bits(t4.w)};
     RowValues rv;
     rv.load<MODE>(a, v);
     float sum[T];
