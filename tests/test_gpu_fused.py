@@ -222,6 +222,33 @@ def test_gated_backward_at_the_ends_of_the_range(cuda_lib, M):
             F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), f"dX {scale} {act}")
 
 
+@pytest.mark.parametrize("M,N,K,G", [(20, 258, 4096, 128), (100, 514, 3968, 32), (300, 1030, 8192, 64)])
+def test_cut_tiles_forward(cuda_lib, M, N, K, G):
+    """Few tiles of a long contraction, cut over the clusters and joined: every mode's epilogue after the join."""
+    pw = F.make_weight(N, K, G, seed=31, far=True)
+    W, X = F.weight64(pw), F.tokens(M, K, 5)
+    bias, residual = _rand((N,), 6), _rand((M, N), 7)
+    F.check(_linear(X, pw, bias, w4.ACT_GELU, residual), *F.linear64(X, W, bias, w4.ACT_GELU, residual), "linear")
+    want, bound, gu, gu_bound = F.gated64(X, W, w4.ACT_SILU)
+    H, GU = _gated(X, pw, w4.ACT_SILU, True)
+    F.check(GU, gu, gu_bound, "GU")
+    F.check(H, want, bound, "H")
+
+
+@pytest.mark.parametrize("M", [20, 100, 300])
+def test_cut_tiles_backward(cuda_lib, M):
+    N, K, act = 8194, 384, w4.ACT_SILU
+    pw = F.make_weight(N, K, 128, seed=32)
+    W, dY = F.weight64(pw), _rand((M, N), 9)
+    F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), W), "dx")
+    dH, GU = _rand((M, N // 2), 3), _rand((M, N), 4, 2.0)
+    d, e = F.grads64(dH, GU, act)
+    dGU, dX = _backward(dH, GU, pw, act)
+    F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, "dGU")
+    want, bound = F.dx64(d, W, r_d=2.0 ** -11, size=F.gated_size(dH, GU))
+    F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), "dX")
+
+
 @pytest.mark.parametrize("M", [20, 90, 300])
 def test_whole_tiles_of_tokens_and_rows_of_every_size(cuda_lib, M):
     """A wave of uncut tiles whose tokens, and whose rows, span FP32's range, beside tiles of ordinary ones."""

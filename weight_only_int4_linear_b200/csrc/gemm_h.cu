@@ -1308,9 +1308,16 @@ int launch_tiles(HArgs a, const CUtensorMap& tx, const CUtensorMap& tq, const CU
     if (units <= 0) return W4A16_ERR_CUDA;
     cfg.numAttrs = 2;
     const int tiles = a.m_tiles * a.r_tiles;
-    // whole waves run whole; a last wave that fills at least nine tenths of the clusters too
+    // Whole waves run whole, and so does a last, partial one where cutting it saves less than it costs.  It saves the
+    // idle clusters' share of a tile's stages, 0.32 us each (backward 0.27); it costs the parts' way through memory and
+    // the join, 0.9 ns per tile and token place and 1 us (backward 2).  Measured, us cut / whole, with 256 tokens, K = 512,
+    // 2048, 4096, 8192: 20 tiles 16.8 / 16.5, 22.5 / 23.8, 27.1 / 33.6, 34.7 / 58.3; 40 tiles 26.0 / 17.6, 31.2 / 25.7,
+    // 38.0 / 38.0, 51.4 / 60.7; 60 tiles 32.9 / 18.6, 40.5 / 28.2, 50.3 / 40.7, 71.0 / 63.3; with 40 tokens and 40 tiles
+    // 12.8 / 11.2, 15.7 / 15.6, 19.8 / 21.7, 27.3 / 34.3.
     int cut = tiles % units;
-    if (cut * 10 >= units * 9) cut = 0;
+    const int64_t saves = (int64_t)(units - cut) * a.NS * (MODE == kDx ? 270 : 320) / units;
+    const int64_t costs = (MODE == kDx ? 2000 : 1000) + (int64_t)cut * NT * 9 / 10;
+    if (saves < costs) cut = 0;
     a.whole_tiles = tiles - cut;
     a.units = units;
     a.base = 1;
