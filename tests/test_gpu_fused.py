@@ -273,6 +273,46 @@ def test_whole_tiles_of_tokens_and_rows_of_every_size(cuda_lib, M):
     F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), F.weight64(pw)), "dx")
 
 
+@pytest.mark.parametrize("M,N", [(3, 18000), (3, 18004), (3, 18002), (40, 9000), (310, 512), (310, 516), (310, 514)])
+def test_gradient_rows_of_every_alignment_shared_by_blocks(cuda_lib, M, N):
+    """Long rows of few tokens (several blocks a token) and short rows of many, in 16-byte, 4-byte and single accesses;
+    shut gates, extreme rows of weights and extreme gradients take the other ways through the preparation."""
+    K, act = 256, w4.ACT_SILU
+    pw = F.make_weight(N, K, 64, seed=41, far=True)
+    for tiny in (False, True):  # 2^-112: powers of two that are no normal FP32 numbers
+        if tiny:
+            pw.scales[3::7] = (pw.scales[3::7].double() * 2.0 ** -112).to(BF)
+        W = F.weight64(pw)
+        for scale in (1.0, 2.0 ** 90):
+            dY = (_rand((M, N), 1).double() * scale).to(BF)
+            F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), W), f"dx {scale} {tiny}")
+            dH, GU = dY[:, : N // 2].contiguous(), _rand((M, N), 2, 2.0)
+            shut = M // 2
+            GU[shut, : N // 2] = -abs(GU[shut, : N // 2]) - 30.0
+            d, e = F.grads64(dH, GU, act)
+            # a shut gate's gradient to a relative 2^-14 of e^x and its factors, as in the test above
+            e[shut] = 2.0 ** -14 * (dH[shut].double().abs() * (1 + GU[shut, : N // 2].double().abs()) ** 3
+                                    * torch.exp(GU[shut, : N // 2].double())).repeat(2) * torch.cat(
+                [GU[shut, N // 2:].double().abs() + 1, torch.ones(N // 2, device="cuda", dtype=F.F8)])
+            e = e + 2.0 ** -126
+            dGU, dX = _backward(dH, GU, pw, act)
+            F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, f"dGU {scale} {tiny}")
+            want, bound = F.dx64(d, W, r_d=2.0 ** -8, size=F.gated_size(dH, GU))
+            F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), f"dX {scale} {tiny}")
+            dGU2, dX2 = _backward(dH, GU.clone(), pw, act, in_place=True)
+            assert torch.equal(dGU2.view(torch.int16), dGU.view(torch.int16))
+            assert torch.equal(dX2.view(torch.int16), dX.view(torch.int16))
+
+
+@pytest.mark.parametrize("N,K,G", [(300, 18560, 32), (520, 9088, 32), (130, 16640, 64)])
+def test_few_rows_of_many_groups(cuda_lib, N, K, G):
+    """The weights' words of few rows: eight rows a block, rows of more groups than a block holds."""
+    pw = F.make_weight(N, K, G, seed=43, far=True)
+    W, X, dY = F.weight64(pw), F.tokens(20, K, 2), _rand((20, N), 3)
+    F.check(_linear(X, pw), *F.linear64(X, W, None, w4.ACT_NONE, None), "forward")
+    F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), W), "dx")
+
+
 def test_tiny_weights_both_ways(cuda_lib):
     N, K = 260, 1024
     pw = F.make_weight(N, K, 128, seed=14)
