@@ -762,14 +762,16 @@ struct Ring {
 // starts inside a tile (its first) and one that starts a tile and does not end it (its last).
 __device__ __forceinline__ int slot_of(int b, int s0) { return 2 * b + (s0 == 0 ? 1 : 0); }
 
-// The residual of T tokens of output row v from token m0 (zero where there is none), loaded ahead of the sums.
+// The residual of T tokens of output row v from token m0 < M on, loaded ahead of the sums: without a branch per token
+// (past the last one it is read again), since eight of them cost more than the rest of a batch's epilogue.
 template <int MODE, int T>
 __device__ __forceinline__ void load_residual(const HArgs& a, int m0, int v, uint16_t (&res)[MODE == kLinear ? T : 1]) {
     if constexpr (MODE == kLinear) {
-        const uint16_t* r = a.ep.residual + (int64_t)m0 * a.R + v;
-        const bool ok = a.ep.residual && v < a.R;
+        if (a.ep.residual == nullptr) return;
+        const uint16_t* r = a.ep.residual + (int64_t)m0 * a.R + min(v, a.R - 1);
+        const int last = a.M - 1 - m0;
 #pragma unroll
-        for (int j = 0; j < T; ++j, r += a.R) res[j] = ok && m0 + j < a.M ? __ldcg(r) : (uint16_t)0;
+        for (int j = 0; j < T; ++j) res[j] = __ldcg(r + (int64_t)min(j, last) * a.R);
     }
 }
 // A token's exponent a as the bits of 2^a where |a| <= kNear, else as a itself.
@@ -1165,7 +1167,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1) gemm_h_kernel(cons
             uint16_t res[MODE == kLinear ? T : 1] = {};
             bool near = false;
             if (whole) {
-                load_residual<MODE, T>(a, m0, v, res);
+                if (m0 < a.M) load_residual<MODE, T>(a, m0, v, res);
                 for (int i = threadIdx.x - C::kEpiWarp * 32; i < NT; i += C::kEpiWarps * 32)
                     s_te[buf][i] = scale_bits(mt * NT + i < a.M ? __ldcg(a.texp + mt * NT + i) : 0);
             }
@@ -1195,7 +1197,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1) gemm_h_kernel(cons
                 for (int j = 0; j < (MODE == kLinear ? T : 1); ++j) rc[j] = res[j];
                 if (cc + T < kCols) {  // the next batch's loads
                     tmem_ld8(tl + buf * NT + c0 + cc + T, d);
-                    if (whole) load_residual<MODE, T>(a, m0 + cc + T, v, res);
+                    if (whole && m0 + cc + T < a.M) load_residual<MODE, T>(a, m0 + cc + T, v, res);
                 } else {
                     tc_fence_before();
                     __syncwarp();
@@ -1252,7 +1254,7 @@ __global__ void __launch_bounds__(kTileRows) gemm_h_join_kernel(const HArgs a) {
         }
     };
     load(first);
-    uint16_t res[MODE == kLinear ? T : 1];
+    uint16_t res[MODE == kLinear ? T : 1] = {};
     load_residual<MODE, T>(a, m0, v, res);
     const int4 t4 = __ldcg(reinterpret_cast<const int4*>(a.texp + m0));
     const int te[T] = {scale_bits(t4.x), scale_bits(t4.y), scale_bits(t4.z), scale_bits(t4.w)};
@@ -1536,6 +1538,7 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
                       reinterpret_cast<uint8_t*>(ws + l.pows), (int)N, (int)l.Rp, a.GQ, 0};
     int st = few_rows(l.Rp) ? launch_pdl(prep_meta_kernel<8>, l.Rp / 8, kPrepThreads, stream, ma)
                             : launch_pdl(prep_meta_kernel<16>, l.Rp / 16, kPrepThreads, stream, ma);
+    if (st != W4A16_OK) return st;
     GradArgs g{};
     g.dY = dY;
     g.dH = dH;
