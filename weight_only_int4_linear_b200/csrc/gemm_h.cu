@@ -30,9 +30,9 @@
 //     the epilogue undoes in its addresses.
 //
 // Work: full waves of tiles run whole, so that the clusters sweep the same
-// operands together (L2); the last, partial wave's tiles are cut along the
-// contraction into equal ranges over all clusters, whose FP32 partial tiles a
-// dependent kernel adds in a fixed order.  With few tokens every tile is cut.
+// operands together (L2); the last, partial wave's tiles, where it pays, are cut
+// along the contraction into equal ranges over all clusters, whose FP32 partial
+// tiles a dependent kernel adds in a fixed order.
 //
 // Gated weights (I gate rows, then I up rows) are read interleaved by a 3-D
 // tensor map, row 2 j + p = row p I + j, so that a pair of neighbouring lanes
@@ -47,7 +47,7 @@
 //
 // What bounds it (1.87 GHz, MMAs of K = 16 measured at 128.5 / 65 / 45 cycles for
 // 256 / 128 / 64 tokens): with 256 tokens the MMAs, 514 of the 516-560 cycles a stage
-// of 64 takes -- 1.51 PFLOP/s on 8192 x 57344 backward and 1.57 forward, 1.74 on
+// of 64 takes -- 1.51 PFLOP/s on 8192 x 57344 backward and 1.58 forward, 1.63-1.74 on
 // 8192 x 10240 backward, until the power limit lowers the clock.  With few tokens the
 // dequantisers: forward 790 cycles per 128 k (2.8 TB/s of codes), backward 490 per 64.
 #include "decode_units.cuh"
