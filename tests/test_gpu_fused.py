@@ -313,6 +313,40 @@ def test_few_rows_of_many_groups(cuda_lib, N, K, G):
     F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), W), "dx")
 
 
+@pytest.mark.parametrize("act", F.ACTS)
+def test_activations_of_every_bf16_value(cuda_lib, act):
+    """One-hot tokens against a weight of one give the activation of each finite BF16 value, and a gated backward pass
+    with dH = U = 1 its derivative.
+
+    e^-|u| is a power of two whose exponent, at most 142 in size before the result vanishes, carries the relative errors
+    of |u| log2 e or x^2 (up to four roundings of 2^-24) and its own rounding of at most 2^-18: in all below 2^-15 of the
+    value."""
+    bits = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16)
+    x = bits.view(BF)
+    x = x[x.double().isfinite()].reshape(-1, 1)
+    M, K = x.shape[0], 128
+    pw = w4.PackedWeight(2, K, device=x.device, group=128)
+    pw.scales.fill_(1.0)
+    pw.zeros.fill_(8)
+    pw.qweight.fill_(-2004318072)  # codes 8
+    pw.qweight[:, 0] += 1
+    X = torch.zeros((M, K), dtype=BF, device="cuda")
+    X[:, :1] = x
+    want = F.act64(x.double(), act).expand(M, 2)
+    e = 2.0 ** -15 * want.abs()
+    F.check(_linear(X, pw, act=act), want, e + F.U16 * (want.abs() + e) + F.TINY, "activation")
+    one = torch.ones_like(x)
+    d, e = F.grads64(one, torch.cat([x, one], 1), act)
+    # 1 / (1 + e^-x) and e^x of x down to -88: |x| 2^-24 log2 e and a few roundings more, as above; x act'(x) terms cancel
+    # to 2^-17 absolutely (grads64)
+    e = e + 2.0 ** -15 * d.abs()
+    dGU = F.nans(M, 2)
+    ws = F.workspace(w4.dx_workspace_bytes(M, 2, K, 128))
+    w4.gated_backward(one, torch.cat([x, one], 1).contiguous(), pw.qweight, pw.scales, pw.zeros, dGU, F.nans(M, K), ws, act=act)
+    _done()
+    F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, "gradients")
+
+
 def test_tiny_weights_both_ways(cuda_lib):
     N, K = 260, 1024
     pw = F.make_weight(N, K, 128, seed=14)
