@@ -510,6 +510,7 @@ template <int W, bool GATED, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs g) {
     using L = Lane8<W, TH>;
     pdl_launch_dependents();
+    if (g.blocks > 1) cluster_sync();  // every block runs before another stores into its shared memory
     pdl_wait_primary();
     RowMax row_max{g.blocks, g.blocks == 1 ? 0 : (int)cluster_ctarank()};
     const int64_t m = blockIdx.x / g.blocks;
