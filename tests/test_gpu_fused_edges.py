@@ -1,0 +1,79 @@
+"""The fused operators where rows or groups of the weight hold nothing but zeros: a zero group or row is stored with a
+scale that says nothing about its values (the quantiser's is 1), and must not decide how the others are scaled."""
+import pytest
+import torch
+
+import weight_only_int4_linear_b200 as w4
+from tests import _fused as F
+from tests.test_gpu_fused import BF, _backward, _dx, _gated, _linear, _rand
+
+pytestmark = pytest.mark.gpu
+
+
+def _sparse_weight(N, K, G, size, seed, symmetric=False):
+    """Weights of one size with rows of zeros as the quantiser stores them, rows whose scales are zero, and rows with one
+    or several zero groups, the first and the last among them."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    W = size * torch.randn((N, K), device="cuda", generator=gen)
+    W[1::5] = 0.0
+    W[3::5, :G] = 0.0
+    W[4::5, K - G:] = 0.0
+    W[4::10, G : 3 * G] = 0.0
+    pw = F.pack(W, G, symmetric)
+    pw.scales[2::15] = 0.0
+    for rows, groups, scale in [(slice(7, None, 35), slice(None), 2.0 ** 20), (slice(9, None, 35), slice(0, 1), 2.0 ** 70)]:
+        pw.zeros[rows, groups], pw.scales[rows, groups] = 8, scale  # pruned after packing: codes 8, any scale
+        pw.qweight.view(N, K // G, G // 8)[rows, groups] = -2004318072
+    return pw
+
+
+SPARSE = [(3, 258, 256, 64), (40, 520, 1024, 128), (100, 130, 384, 32), (310, 514, 512, 64), (20, 70, 18560, 32)]
+
+
+@pytest.mark.parametrize("M,N,K,G", SPARSE)
+@pytest.mark.parametrize("size", [1e-2, 1e-6, 1e-10])
+@pytest.mark.parametrize("symmetric", [False, True])
+def test_gradients_beside_rows_and_groups_of_zeros(cuda_lib, M, N, K, G, size, symmetric):
+    pw = _sparse_weight(N, K, G, size, N + K, symmetric)
+    W = F.weight64(pw)
+    dead = (W == 0).all(1)
+    assert int(dead.sum()) >= N // 5
+    dY = _rand((M, N), 1, 1e-3)
+    dY[:, dead] *= 2.0 ** 12  # the largest gradients belong to rows that add nothing
+    F.check(_dx(dY, pw), *F.dx64(dY.to(F.F8), W), "dx")
+    act = w4.ACT_SILU
+    dH, GU = dY[:, : N // 2].contiguous(), _rand((M, N), 2, 2.0)
+    d, e = F.grads64(dH, GU, act)
+    dGU, dX = _backward(dH, GU, pw, act)
+    F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, "dGU")
+    want, bound = F.dx64(d, W, r_d=2.0 ** -11, size=F.gated_size(dH, GU))
+    F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), "dX")
+
+
+@pytest.mark.parametrize("M,N,K,G", SPARSE + [(1, 258, 1024, 128), (7, 258, 1024, 128), (1, 258, 512, 32)])
+@pytest.mark.parametrize("size", [1e-2, 1e-9, 1e-11])
+@pytest.mark.parametrize("symmetric", [False, True])
+def test_forward_beside_groups_of_zeros(cuda_lib, M, N, K, G, size, symmetric):
+    pw = _sparse_weight(N, K, G, size, N + K, symmetric)
+    W, X = F.weight64(pw), F.tokens(M, K, 3)
+    F.check(_linear(X, pw), *F.linear64(X, W, None, w4.ACT_NONE, None), "linear")
+    want, bound, gu, gu_bound = F.gated64(X, W, w4.ACT_NONE)
+    H, GU = _gated(X, pw, w4.ACT_NONE, True)
+    F.check(GU, gu, gu_bound, "GU")
+    F.check(H, want, bound, "H")
+
+
+@pytest.mark.parametrize("M", [5, 70])
+def test_a_weight_of_zeros_and_one_live_row(cuda_lib, M):
+    N, K = 258, 1024
+    zero = F.pack(torch.zeros((N, K), device="cuda"), 128)
+    dY = _rand((M, N), 1)
+    assert not _dx(dY, zero).any() and not _linear(F.tokens(M, K, 2), zero).any()
+    W = torch.zeros((N, K), device="cuda")
+    W[N - 1, K - 1] = 1e-8  # the last value of the last group
+    one = F.pack(W, 128)
+    F.check(_dx(dY, one), *F.dx64(dY.to(F.F8), F.weight64(one)), "one value")
+    far = F.pack(W + 0.0, 128)
+    far.scales[0], far.zeros[0] = 2.0 ** -60, 5000  # beside a row whose zero points are far beyond the codes
+    F.check(_dx(dY, far), *F.dx64(dY.to(F.F8), F.weight64(far)), "far zero points")

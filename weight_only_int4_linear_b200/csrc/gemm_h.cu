@@ -164,15 +164,23 @@ constexpr int kPrepThreads = 256;
 // (1097 x 28416 in groups of 32: 23 us with 16 rows).
 constexpr int kMetaWords = 4096;  // held in shared memory at a time: a block's rows of 256 or 512 groups
 
+//
+// A group whose codes all equal its zero point holds only zeros, and its scale says nothing about them (the quantiser
+// stores 1): it must not set the exponent.  Codes are read where that could matter: in rows whose groups' bounds lie more
+// than 2^kSpread apart, and backward, where a row of zeros would scale its token's whole gradient, in rows whose first
+// eight codes are zeros.  A group then left above the row's exponent is one of zeros, and its word is 0.
 struct MetaArgs {
+    const uint32_t* qweight;
     const uint16_t* scales;
     const int32_t* zeros;
     uint32_t* meta;
-    int16_t* exps;  // [Rp] e
-    uint8_t* pows;  // [Rp] e + 127 (backward): the FP32 exponent field of 2^e, 0 where that is no normal number
-    int R, Rp, GQ;
-    int64_t I;      // gated: rows per half, else 0
+    int16_t* exps;  // [Rp] e; kZeroRow (backward) for a row of zeros
+    uint8_t* pows;  // [Rp] (backward) the FP32 exponent field of 2^e: 0 for a row of zeros, 255 where 2^e is no normal number
+    int R, Rp, GQ, words;  // words: of codes per group
+    int64_t I;             // gated: rows per half, else 0
 };
+constexpr int kSpread = 4;
+constexpr int kZeroRow = -32768, kLeastExp = -10000;  // kLeastExp: between kZeroRow's sums and those of any other row
 
 __device__ __forceinline__ int bf16_exponent(uint32_t bits) {  // floor(log2 |x|), or above it for subnormals
     const int ef = (int)((bits >> 7) & 0xFF);
@@ -180,8 +188,39 @@ __device__ __forceinline__ int bf16_exponent(uint32_t bits) {  // floor(log2 |x|
 }
 constexpr int kNothing = -100000;  // exponent of zero
 
+// Exponent bound of a group: its values are below 2^bound.  |q - z| <= max(|z|, |15 - z|) < 2^bits.
+__device__ __forceinline__ int group_bound(uint32_t scale, int z) {
+    if ((scale & 0x7FFFu) == 0) return kNothing;
+    const uint32_t mag = z < 8 ? 15u - (uint32_t)z : (uint32_t)z;
+    return bf16_exponent(scale) + 1 + ((uint32_t)z < 16u ? 4 : 32 - __clz(mag));
+}
+
+// The largest bound, from t down, of a row's groups that hold a value other than zero; called by a whole warp.
+__device__ __noinline__ int live_bound(const uint4* codes, const uint16_t* scales, const int32_t* zeros, int groups,
+                                       int quads, int t) {
+    const int lane = threadIdx.x & 31;
+    while (t != kNothing) {
+        bool live = false;
+        int next = kNothing;  // the largest bound below t
+        for (int g = lane; g < groups; g += 32) {
+            const int z = __ldg(zeros + g), b = group_bound(__ldg(scales + g), z);
+            if (b < t) next = max(next, b);
+            if (b != t || live) continue;
+            live = (uint32_t)z >= 16u;
+            for (int i = 0; i < quads && !live; ++i) {
+                const uint4 v = __ldg(codes + (int64_t)g * quads + i);
+                const uint32_t zero = 0x11111111u * (uint32_t)z;
+                live = v.x != zero || v.y != zero || v.z != zero || v.w != zero;
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, live)) return t;
+        t = __reduce_max_sync(0xFFFFFFFFu, next);
+    }
+    return t;
+}
+
 // Rows of up to kMetaWords / ROWS groups are read once: scale and zero point wait in shared memory for the row's exponent.
-template <int ROWS>
+template <int ROWS, bool BACK>
 __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
     constexpr int kMetaGroups = kMetaWords / ROWS;
     __shared__ uint32_t s_raw[ROWS][kMetaGroups + 1];  // scale bits, zero point << 16 (0x7FFF: beyond 1024)
@@ -190,14 +229,18 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int v0 = block * ROWS, r0 = warp * RW;
     int64_t first[RW];  // the row's first group, -1 past the matrix
-    int top[RW];         // exponent bound of the row's values: |s| < 2^(exponent + 1) times the zero point's part
-    uint32_t usual[RW];  // largest scale of the groups with a zero point in 0 .. 15, where |q - z| < 2^4
+    int top[RW], low[RW];  // largest and smallest exponent bound of the row's groups
+    uint32_t usual[RW], least[RW];  // largest and smallest scale of the groups with a zero point in 0 .. 15
+    uint32_t word[RW];     // backward: the row's first codes
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
         const int v = v0 + r0 + i;
         first[i] = v < a.R ? (a.I ? gated_row(v, a.I) : (int64_t)v) * a.GQ : -1;
         top[i] = kNothing;
+        low[i] = -kNothing;
         usual[i] = 0u;
+        least[i] = 0xFFFFFFFFu;
+        word[i] = BACK && v < a.R ? __ldg(a.qweight + first[i] * a.words) : 0u;
     }
     // groups g0 .. g1 - 1 of the warp's rows into shared memory, U groups of each in flight per lane
     auto read = [&](int g0, int g1) {
@@ -222,9 +265,11 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
                     uint32_t zw = (uint32_t)zz << 16;
                     if ((uint32_t)zz < 16u) {
                         usual[i] = max(usual[i], sb[i][l] & 0x7FFFu);
-                    } else {  // |q - z| <= max(|z|, |15 - z|) < 2^bits
-                        const uint32_t mag = zz < 8 ? 15u - (uint32_t)zz : (uint32_t)zz;
-                        if (sb[i][l] & 0x7FFFu) top[i] = max(top[i], bf16_exponent(sb[i][l]) + 1 + (32 - __clz(mag)));
+                        least[i] = min(least[i], sb[i][l] & 0x7FFFu);
+                    } else {
+                        const int b = group_bound(sb[i][l], zz);
+                        top[i] = max(top[i], b);
+                        low[i] = min(low[i], b);
                         if (zz < -1024 || zz > 1024) zw = 0x7FFF0000u;
                     }
                     s_raw[r0 + i][g - g0] = sb[i][l] | zw;
@@ -232,15 +277,29 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
         }
     };
     for (int g0 = 0; g0 < a.GQ; g0 += kMetaGroups) read(g0, min(g0 + kMetaGroups, a.GQ));
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        if (usual[i]) top[i] = max(top[i], bf16_exponent(usual[i]) + 1 + 4);
-        const int t = __reduce_max_sync(0xFFFFFFFFu, top[i]), e = t == kNothing ? 0 : t - kTopExp;
+        if (least[i] <= 0x7FFFu) {
+            top[i] = max(top[i], group_bound(usual[i], 0));
+            low[i] = min(low[i], group_bound(least[i], 0));  // kNothing for a scale of 0: the row is looked at
+        }
+        int t = __reduce_max_sync(0xFFFFFFFFu, top[i]);
+        bool look = t - __reduce_min_sync(0xFFFFFFFFu, low[i]) > kSpread;
+        if (BACK && first[i] >= 0) {
+            const uint32_t z0 = a.GQ <= kMetaGroups ? s_raw[r0 + i][0] >> 16 : (uint32_t)__ldg(a.zeros + first[i]);
+            look = look || word[i] == 0x11111111u * z0;
+        }
+        if (look)
+            t = live_bound(reinterpret_cast<const uint4*>(a.qweight + first[i] * a.words), a.scales + first[i],
+                           a.zeros + first[i], a.GQ, a.words / 4, t);
+        const int e = t == kNothing ? 0 : t - kTopExp;
         if (lane == 0) {
             const int v = v0 + r0 + i;
+            const bool none = BACK && t == kNothing;
             s_exp[r0 + i] = e;
-            a.exps[v] = (int16_t)e;
-            if (a.pows) a.pows[v] = (uint8_t)(e >= -126 && e <= 127 ? e + 127 : 0);
+            a.exps[v] = (int16_t)(none ? kZeroRow : e);
+            if (BACK) a.pows[v] = (uint8_t)(none ? 0 : e >= -126 && e <= 127 ? e + 127 : 255);
         }
     }
     for (int g0 = 0; g0 < a.GQ; g0 += kMetaGroups) {
@@ -253,21 +312,23 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
         const int rr = lane % ROWS, gs = lane / ROWS;  // row, and group within the warp's
         constexpr int GW = 32 / ROWS;
         const int e = s_exp[rr];
-        // A positive scale whose 2^-e multiple is a normal FP16 number, and a zero point in 0 .. 1023: the word by
-        // integer arithmetic on the formats' fields (exponent bias 127 -> 15, 7 -> 10 mantissa bits; 1024 + z is
-        // 0x6400 + z).  Else by conversions.
+        // A positive scale whose 2^-e multiple is a normal FP16 number below 2^11, as that of every group within the row's
+        // bound, and a zero point in 0 .. 1023: the word by integer arithmetic on the formats' fields (exponent bias
+        // 127 -> 15, 7 -> 10 mantissa bits; 1024 + z is 0x6400 + z).  Else by conversions.
         const int bias = (15 - 127 - e) * 1024;
         uint32_t* out = a.meta + (int64_t)(g0 + warp * GW + gs) * a.Rp + v0 + rr;
         for (int g = warp * GW + gs; g < g1 - g0; g += kPrepThreads / ROWS, out += (int64_t)(kPrepThreads / ROWS) * a.Rp) {
             const uint32_t raw = s_raw[rr][g];
             const int h = (int)((raw & 0xFFFFu) << 3) + bias;
             uint32_t word = (uint32_t)h + (raw & 0xFFFF0000u) + 0x64000000u;
-            if (h < 0x400 || h > 0x7BFF || (raw & 0x8000u) || raw >= (1024u << 16)) {
+            if (h < 0x400 || h >= 0x6800 || (raw & 0x8000u) || raw >= (1024u << 16)) {
                 const int z = (int)raw >> 16;
                 const float s = scale2(bf16_bits_to_float((uint16_t)raw), -e);
                 word = z != 0x7FFF ? (uint32_t)__half_as_ushort(__float2half_rn(s)) |
                                          ((uint32_t)__half_as_ushort(__int2half_rn(1024 + z)) << 16)
                                    : ((uint32_t)e & 0xFFFFu) | 0x7FFF0000u;
+                // above the row's bound: a group of zeros (codes of 0 .. 15 alone can all be the zero point)
+                if ((uint32_t)z < 16u && fabsf(s) >= 2048.f && (raw & 0x7F80u) != 0x7F80u) word = 0u;
             }
             *out = v0 + rr < a.R ? word : 0u;
         }
@@ -309,7 +370,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_forward_kernel(const MetaAr
     pdl_wait_primary();  // X of an earlier kernel; the workspace's earlier readers
     const int m = blockIdx.x;
     if (m >= t.M) {
-        meta_block<ROWS>(ma, m - t.M);
+        meta_block<ROWS, false>(ma, m - t.M);
         return;
     }
     const uint4* x = reinterpret_cast<const uint4*>(t.X + (int64_t)m * t.K);
@@ -361,7 +422,7 @@ template <int ROWS>
 __global__ void __launch_bounds__(kPrepThreads) prep_meta_kernel(const MetaArgs ma) {
     pdl_launch_dependents();
     pdl_wait_primary();
-    meta_block<ROWS>(ma, blockIdx.x);
+    meta_block<ROWS, true>(ma, blockIdx.x);
 }
 
 // Backward preparation, one block per token: the FP16 operand D'[m][n] = dY[m][n] 2^(e_n - a_m), row stride Np.
@@ -379,8 +440,8 @@ struct GradArgs {
     const uint16_t* dH;
     const uint16_t* GU;
     uint16_t* dGU;
-    const int16_t* exps;  // [>= N] e_n
-    const uint8_t* pows;  // [>= N] exponent field of 2^e_n, or 0
+    const int16_t* exps;  // [>= N] e_n, kZeroRow for a row of zeros
+    const uint8_t* pows;  // [>= N] exponent field of 2^e_n: 0 for a row of zeros, 255 where 2^e_n is no normal number
     __half* Dh;
     int* texp;
     int N, I, act;
@@ -521,7 +582,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
     const uint16_t* gu = GATED ? g.GU + m * g.N : nullptr;
     uint16_t* dgu = GATED ? g.dGU + m * g.N : nullptr;
 
-    float bound = 0.f, least = 1.f;
+    float bound = 0.f, most_p = 1.f;  // a row of zeros (p = 0) adds nothing to the bound
 #pragma unroll 2
     for (int s = row_max.rank; s < steps; s += g.blocks) {
         const int i = L::first(s);
@@ -537,19 +598,19 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 bound = fmaxf(bound, fmaxf(fabsf(2.f * d[j] * uu[j]) * p[j], fabsf(d[j] * gg[j]) * q[j]));
-                least = fminf(least, fminf(p[j], q[j]));
+                most_p = fmaxf(most_p, fmaxf(p[j], q[j]));
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 bound = fmaxf(bound, fabsf(d[j]) * p[j]);
-                least = fminf(least, p[j]);
+                most_p = fmaxf(most_p, p[j]);
             }
         }
     }
-    // fast: every 2^e a normal number (else 1000 stands for the bound), and the bound so far inside FP32's range that
-    // neither 2^e nor the values that matter (down to 2^-40 of it) can leave it
-    const int E = row_max(least > 0.f ? exp_of(bound) : 1000);
+    // fast: every 2^e a normal number (else, p infinite, 1000 stands for the bound), and the bound so far inside FP32's
+    // range that neither 2^e nor the values that matter (down to 2^-40 of it) can leave it
+    const int E = row_max(most_p < __int_as_float(0x7F800000) ? exp_of(bound) : 1000);
     const bool fast = E >= -70 && E < 100;
 
     // values of step s: dG, dU (or dY in v)
@@ -635,7 +696,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = max(top, max(exp_of(v[j]) + ev[j], exp_of(u[j]) + eu[j]));
         });
-        top = row_max(top < kNothing / 2 ? kNothing : top);
+        top = row_max(top < kLeastExp ? kNothing : top);
         const int a = row_exp(top);
         if (threadIdx.x == 0 && row_max.rank == 0) g.texp[m] = a;
         each([&](int i, float (&v)[8], float (&u)[8], int (&ev)[8], int (&eu)[8]) {
@@ -663,7 +724,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = max(top, exp_of(d[j]) + e[j]);
         }
-        top = row_max(top < kNothing / 2 ? kNothing : top);
+        top = row_max(top < kLeastExp ? kNothing : top);
         const int a = row_exp(top);
         if (threadIdx.x == 0 && row_max.rank == 0) g.texp[m] = a;
         for (int s = row_max.rank; s < steps; s += g.blocks) {
@@ -1488,8 +1549,8 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     if (!ok || !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
                                (uint64_t)l.Rp * 4, kBM, stage_k > (uint32_t)group ? stage_k / (uint32_t)group : 1))
         return W4A16_ERR_CUDA;
-    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int16_t*>(ws + l.exps),
-                      nullptr, (int)N, (int)l.Rp, a.GQ, I};
+    const MetaArgs ma{qweight, scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta),
+                      reinterpret_cast<int16_t*>(ws + l.exps), nullptr, (int)N, (int)l.Rp, a.GQ, group / 8, I};
     const TokenArgs t{X, xscale, reinterpret_cast<__half*>(ws + l.op), reinterpret_cast<int*>(ws + l.texp), (int)M,
                       (int)K};
     const int st = few_rows(l.Rp) ? launch_pdl(prep_forward_kernel<8>, l.Rp / 8 + M, kPrepThreads, stream, ma, t)
@@ -1535,8 +1596,9 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
         !encode_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws + l.meta, (uint64_t)l.Rp, (uint64_t)a.GQ,
                         (uint64_t)l.Rp * 4, kBK, (uint32_t)(kBM / group)))
         return W4A16_ERR_CUDA;
-    const MetaArgs ma{scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta), reinterpret_cast<int16_t*>(ws + l.exps),
-                      reinterpret_cast<uint8_t*>(ws + l.pows), (int)N, (int)l.Rp, a.GQ, 0};
+    const MetaArgs ma{qweight, scales, zeros, reinterpret_cast<uint32_t*>(ws + l.meta),
+                      reinterpret_cast<int16_t*>(ws + l.exps), reinterpret_cast<uint8_t*>(ws + l.pows), (int)N, (int)l.Rp,
+                      a.GQ, group / 8, 0};
     int st = few_rows(l.Rp) ? launch_pdl(prep_meta_kernel<8>, l.Rp / 8, kPrepThreads, stream, ma)
                             : launch_pdl(prep_meta_kernel<16>, l.Rp / 16, kPrepThreads, stream, ma);
     if (st != W4A16_OK) return st;
