@@ -1,5 +1,7 @@
-"""The fused operators where rows or groups of the weight hold nothing but zeros: a zero group or row is stored with a
-scale that says nothing about its values (the quantiser's is 1), and must not decide how the others are scaled."""
+"""The fused operators at the edges of their inputs: rows and groups of the weight that hold nothing but zeros, sums that
+are NaN or past FP32's range."""
+import math
+
 import pytest
 import torch
 
@@ -10,6 +12,8 @@ from tests.test_gpu_fused import BF, _backward, _dx, _gated, _linear, _rand
 pytestmark = pytest.mark.gpu
 
 
+# A zero group or row is stored with a scale that says nothing about its values (the quantiser's is 1): it must not decide
+# how the others are scaled.
 def _sparse_weight(N, K, G, size, seed, symmetric=False):
     """Weights of one size with rows of zeros as the quantiser stores them, rows whose scales are zero, and rows with one
     or several zero groups, the first and the last among them."""
@@ -77,3 +81,31 @@ def test_a_weight_of_zeros_and_one_live_row(cuda_lib, M):
     far = F.pack(W + 0.0, 128)
     far.scales[0], far.zeros[0] = 2.0 ** -60, 5000  # beside a row whose zero points are far beyond the codes
     F.check(_dx(dY, far), *F.dx64(dY.to(F.F8), F.weight64(far)), "far zero points")
+
+
+@pytest.mark.parametrize("act", F.ACTS)
+@pytest.mark.parametrize("M", [1, 5, 40, 300])
+def test_not_a_number_reaches_the_output(cuda_lib, M, act):
+    """A sum that is NaN stays NaN through every activation, and its neighbours keep their values."""
+    N, K = 300, 1024
+    pw = F.make_weight(N, K, 128, seed=act)
+    X, bias = F.tokens(M, K, act), _rand(N, 5)
+    plain = _linear(X, pw, bias, act)
+    bias[::7] = math.nan
+    Y = _linear(X, pw, bias, act)
+    assert torch.equal(Y.isnan(), bias.isnan().expand(M, N))
+    assert torch.equal(Y[:, ~bias.isnan()], plain[:, ~bias.isnan()])
+
+
+@pytest.mark.parametrize("act", F.ACTS)
+def test_a_token_that_is_not_a_number_through_the_gate(cuda_lib, act):
+    M, N, K = 40, 258, 640  # tokens of the GEMM (the integer GEMVs take finite values only)
+    pw = F.make_weight(N, K, 128, seed=act)
+    X = F.tokens(M, K, act)
+    X[3, 7] = math.nan
+    H, GU = _gated(X, pw, act, True)
+    assert bool(H[3].isnan().all()) and bool(GU[3].isnan().all())
+    X[3, 7] = 0.0
+    keep = torch.arange(M, device="cuda") != 3
+    again, _ = _gated(X, pw, act, True)
+    assert torch.equal(H[keep], again[keep])

@@ -73,6 +73,12 @@ __device__ __forceinline__ float rcp_f(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// max(x, 0), NaN for NaN (fmaxf gives the other operand).
+__device__ __forceinline__ float max0_nan(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // The activations of a pair, with one exponential e^-|u| each.  It is taken 2^16 times larger, so that it flushes to
 // zero only where the result is below half of BF16's smallest step; adding 16 to its exponent costs 2^-20.5 of it.
@@ -107,8 +113,8 @@ __device__ __forceinline__ void gelu2(float& x, float& y) {
     for (int i = 6; i >= 0; --i) r = fma2(r, t, pack2(kTail[i] * 0x1p-16f, kTail[i] * 0x1p-16f));
     float g, h;
     unpack2(mul2(pack2(ex2_f(d), ex2_f(e)), r), g, h);
-    x = fmaf(-ax, g, fmaxf(x, 0.f));
-    y = fmaf(-ay, h, fmaxf(y, 0.f));
+    x = fmaf(-ax, g, max0_nan(x));  // ax is 16 for NaN
+    y = fmaf(-ay, h, max0_nan(y));
 }
 
 // x[j] = act(x[j]), T even; the choice is uniform over the grid.
