@@ -109,3 +109,33 @@ def test_a_token_that_is_not_a_number_through_the_gate(cuda_lib, act):
     keep = torch.arange(M, device="cuda") != 3
     again, _ = _gated(X, pw, act, True)
     assert torch.equal(H[keep], again[keep])
+
+
+@pytest.mark.parametrize("act", F.ACTS)
+@pytest.mark.parametrize("M", [1, 5, 40, 300])
+def test_infinite_sums_give_the_limit(cuda_lib, M, act):
+    N, K = 300, 1024
+    pw = F.make_weight(N, K, 128, seed=act)
+    X, bias = F.tokens(M, K, act), _rand(N, 5)
+    plain = _linear(X, pw, bias, act)
+    bias[100], bias[299] = -math.inf, math.inf
+    Y = _linear(X, pw, bias, act)
+    assert bool((Y[:, 100] == (-math.inf if act == w4.ACT_NONE else 0.0)).all()), Y[:, 100]
+    assert bool((Y[:, 299] == math.inf).all())
+    keep = bias.isfinite()
+    assert torch.equal(Y[:, keep], plain[:, keep])
+
+
+@pytest.mark.parametrize("act", F.ACTS[1:])
+@pytest.mark.parametrize("M", [1, 5, 40, 300])
+def test_gate_sums_below_the_range(cuda_lib, M, act):
+    """Finite inputs whose gate sum is below FP32's range: the gate is shut, H is 0."""
+    N, K = 130, 1024
+    I = N // 2
+    W = 0.02 * torch.rand((N, K), device="cuda") + 0.01
+    W[:I] *= 2.0 ** 20
+    pw = F.pack(W, 128)
+    X = torch.full((M, K), -(2.0 ** 110), dtype=BF, device="cuda")
+    H, GU = _gated(X, pw, act, True)
+    assert bool((GU[:, :I] == -math.inf).all()) and bool(GU[:, I:].isfinite().all())
+    assert bool((H == 0).all()), H

@@ -6,6 +6,8 @@
 
 #include "../../include/w4a16_fused.h"
 
+#include <cfloat>
+
 namespace w4a16 {
 
 // What follows the product X . W_hat^T.  gated == 0: Y = act(sum + bias) + residual, each optional.
@@ -84,14 +86,16 @@ __device__ __forceinline__ float max0_nan(float x) {
 // zero only where the result is below half of BF16's smallest step; adding 16 to its exponent costs 2^-20.5 of it.
 //   x sigmoid(u), u of x's sign, t = e^-|u|:  (max(x, 0) + min(x, 0) t) / (1 + t)      (SILU: u = x)
 //   x Phi(x), tail h = Phi(-|x|):             max(x, 0) - |x| h                        (zero from |x| = 16 on)
-// None cancels for negative x.
+// None cancels for negative x.  min(x, 0) ends at FP32's lowest number, so that an overflowed sum of -infinity gives the
+// limit 0 and not infinity times zero.
 constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float finite_min0(float x) { return fmaxf(fminf(x, 0.f), -FLT_MAX); }
 __device__ __forceinline__ uint64_t x_sigmoid2(float x, float y, float u, float v) {
     const uint64_t t = pack2(ex2_f(fmaf(-fabsf(u), kLog2e, 16.f)), ex2_f(fmaf(-fabsf(v), kLog2e, 16.f)));
     const uint64_t down = pack2(0x1p-16f, 0x1p-16f);
     float d, e;
     unpack2(fma2(t, down, pack2(1.f, 1.f)), d, e);
-    const uint64_t n = fma2(mul2(pack2(fminf(x, 0.f), fminf(y, 0.f)), t), down, pack2(fmaxf(x, 0.f), fmaxf(y, 0.f)));
+    const uint64_t n = fma2(mul2(pack2(finite_min0(x), finite_min0(y)), t), down, pack2(fmaxf(x, 0.f), fmaxf(y, 0.f)));
     return mul2(n, pack2(rcp_f(d), rcp_f(e)));
 }
 __device__ __forceinline__ void silu2(float& x, float& y) { unpack2(x_sigmoid2(x, y, x, y), x, y); }
