@@ -139,3 +139,40 @@ def test_gate_sums_below_the_range(cuda_lib, M, act):
     H, GU = _gated(X, pw, act, True)
     assert bool((GU[:, :I] == -math.inf).all()) and bool(GU[:, I:].isfinite().all())
     assert bool((H == 0).all()), H
+
+
+@pytest.mark.parametrize("M,N", [(3, 258), (70, 514), (310, 512), (3, 18000)])
+@pytest.mark.parametrize("act", F.ACTS)
+def test_gated_gradients_whose_first_product_leaves_the_range(cuda_lib, M, N, act):
+    """dH U past FP32's largest number under a gate that brings the gradient back or shuts it, also where the weight's row
+    is zero, in the first token; the last token's ends of the range meet a gate of ordinary size."""
+    K, I = 256, N // 2
+    pw = F.make_weight(N, K, 64, seed=17)
+    pw.scales[3] = 0.0
+    pw.scales[I + 2] = 0.0
+    W = F.weight64(pw)
+    dH, GU = _rand((M, I), 1), _rand((M, N), 2, 2.0)
+    gates = {w4.ACT_SILU: [-30000.0, -3.0, -60.0, -70.0], w4.ACT_GELU: [-30000.0, -3.0, -10.5, -11.0],
+             w4.ACT_GELU_TANH: [-30000.0, -3.0, -8.7, -9.0]}.get(act, [-1.0, -3.0, -8.0, -9.0])
+    GU[0, :4] = torch.tensor(gates, device="cuda").to(BF)
+    dH[0, :4] = torch.tensor([2.0 ** 60, 2.0 ** 60, 2.0 ** 100, 2.0 ** 100], device="cuda").to(BF)
+    GU[0, I : I + 4] = torch.tensor([2.0 ** 100, -(2.0 ** 60), 2.0 ** 100, -(2.0 ** 100)], device="cuda").to(BF)
+    if act == w4.ACT_NONE:
+        GU[0, I : I + 4] = 2.0 ** 20
+    dH[M - 1, I - 1], GU[M - 1, I - 1] = 3e36 if act == w4.ACT_NONE else 3e38, -1.0
+    GU[M - 1, N - 1] = 3.3e38 if act == w4.ACT_RELU else 0.5
+    d, e = F.grads64(dH, GU, act)
+    assert bool((d.abs() < 3e38).all())
+    # FP32 holds a shut gate's gradients to a relative 2^-11: differences of two terms of e^x, x off by |x| 2^-22 at most
+    for part in (slice(0, 4), slice(I, I + 4)):
+        e[0, part] = 2.0 ** -11 * d[0, part].abs()
+    if act == w4.ACT_RELU:
+        e[M - 1] = 0.0  # the factors are 0 and 1
+    dGU, dX = _backward(dH, GU, pw, act)
+    F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, "dGU")
+    size = F.gated_size(dH, GU)
+    size[[0, M - 1]] = d[[0, M - 1]].abs()  # at the ends of the range a token is scaled by its gradients themselves
+    want, bound = F.dx64(d, W, r_d=2.0 ** -11, size=size)
+    F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), "dX")
+    dGU2, dX2 = _backward(dH, GU.clone(), pw, act, in_place=True)
+    assert torch.equal(dGU2, dGU) and torch.equal(dX2, dX)

@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
     const uint16_t* gu = GATED ? g.GU + m * g.N : nullptr;
     uint16_t* dgu = GATED ? g.dGU + m * g.N : nullptr;
 
-    float bound = 0.f, most_p = 1.f;  // a row of zeros (p = 0) adds nothing to the bound
+    float bound = 0.f, most_f = 1.f;  // a row of zeros (p = 0) adds nothing to the bound; most_f: the largest factor
 #pragma unroll 2
     for (int s = row_max.rank; s < steps; s += g.blocks) {
         const int i = L::first(s);
@@ -597,20 +597,23 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
             L::load_pows(g.pows + g.I, i, n, q);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                bound = fmaxf(bound, fmaxf(fabsf(2.f * d[j] * uu[j]) * p[j], fabsf(d[j] * gg[j]) * q[j]));
-                most_p = fmaxf(most_p, fmaxf(p[j], q[j]));
+                const float b = fabsf(2.f * d[j] * uu[j]), c = fabsf(d[j] * gg[j]);
+                bound = fmaxf(bound, fmaxf(b * p[j], c * q[j]));
+                most_f = fmaxf(fmaxf(most_f, fmaxf(b, c)), fmaxf(p[j], q[j]));
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 bound = fmaxf(bound, fabsf(d[j]) * p[j]);
-                most_p = fmaxf(most_p, p[j]);
+                most_f = fmaxf(most_f, p[j]);
             }
         }
     }
-    // fast: every 2^e a normal number (else, p infinite, 1000 stands for the bound), and the bound so far inside FP32's
-    // range that neither 2^e nor the values that matter (down to 2^-40 of it) can leave it
-    const int E = row_max(most_p < __int_as_float(0x7F800000) ? exp_of(bound) : 1000);
+    // fast: every 2^e a normal number (else p is infinite), dH U and dH G inside FP32's range (1000 stands for the bound
+    // where one is not), and the bound so far inside it that neither 2^e nor the values that matter (down to 2^-40 of it)
+    // can leave it
+    constexpr float kInf = __builtin_huge_valf();
+    const int E = row_max(most_f < kInf ? exp_of(bound) : 1000);
     const bool fast = E >= -70 && E < 100;
 
     // values of step s: dG, dU (or dY in v)
@@ -624,7 +627,9 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
             act_grads<8>(gg, g.act, u, v);  // u = act, v = act'
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[j] *= d[j] * uu[j];
+                const float t = d[j] * uu[j];
+                // outside the range act' comes first, with half of U (|act'| <= 1.13), so that only dG itself overflows
+                v[j] = fast || fabsf(t) < kInf ? v[j] * t : v[j] * (0.5f * uu[j]) * d[j] * 2.f;
                 u[j] *= d[j];
             }
         } else {
@@ -706,8 +711,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH) prep_grad_kernel(const GradArgs
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[j] = scale2(v[j], ev[j] - a);
-                u[j] = scale2(u[j], eu[j] - a);
+                v[j] = ev[j] == kZeroRow ? 0.f : scale2(v[j], ev[j] - a);  // a gradient past the range too adds nothing
+                u[j] = eu[j] == kZeroRow ? 0.f : scale2(u[j], eu[j] - a);
             }
             L::store_half(out, i, n, v);
             L::store_half(out + g.I, i, n, u);
