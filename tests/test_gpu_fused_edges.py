@@ -176,3 +176,17 @@ def test_gated_gradients_whose_first_product_leaves_the_range(cuda_lib, M, N, ac
     F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()), "dX")
     dGU2, dX2 = _backward(dH, GU.clone(), pw, act, in_place=True)
     assert torch.equal(dGU2, dGU) and torch.equal(dX2, dX)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 258, 256), (40, 8194, 384), (300, 130, 1024), (20, 130, 19456)])
+@pytest.mark.parametrize("up", [False, True])
+def test_channel_scales_bring_gradients_back_into_the_range(cuda_lib, M, N, K, up):
+    """Sums past FP32's range, or below its smallest number, that the channel's scale brings back."""
+    pw = F.make_weight(N, K, 128, seed=19)
+    pw.scales.copy_((pw.scales.double() * 2.0 ** (-30 if up else 10)).to(BF))
+    W = F.weight64(pw)
+    dY = (_rand((M, N), 1).double() * 2.0 ** (-125 if up else 120)).to(BF)
+    inv = torch.exp2(torch.linspace(-2, 2, K, device="cuda")) * 2.0 ** (60 if up else -40)
+    want, bound = F.dx64(dY.to(F.F8), W, inv)
+    assert 1e-30 < float(want.abs().max()) < 1e38
+    F.check(_dx(dY, pw, inv), want, bound)

@@ -138,12 +138,12 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// x 2^t: two exact factors, so that only the result can leave the FP32 range.  Past +-252 the callers' results are
-// zero or infinite either way.
-__device__ __forceinline__ float scale2(float x, int t) {
+// x f 2^t: the power in two exact factors around f, so that only the result can leave the FP32 range.  Past +-252 the
+// callers' results are zero or infinite either way.
+__device__ __forceinline__ float scale2(float x, int t, float f = 1.f) {
     t = min(max(t, -252), 252);
     const int h = t >> 1;
-    return x * __uint_as_float((uint32_t)(h + 127) << 23) * __uint_as_float((uint32_t)(t - h + 127) << 23);
+    return x * __uint_as_float((uint32_t)(h + 127) << 23) * f * __uint_as_float((uint32_t)(t - h + 127) << 23);
 }
 
 // FP32 -> BF16 bits, nearest even, as one conversion instruction.
@@ -895,8 +895,7 @@ __device__ __forceinline__ void finish(const HArgs& a, float (&y)[T], const int 
     } else {
 #pragma unroll
         for (int j = 0; j < T; ++j) {
-            y[j] = scale2(y[j], r.e + scale_exp(te[j]));
-            if (MODE == kDx) y[j] *= r.col_s;
+            y[j] = scale2(y[j], r.e + scale_exp(te[j]), MODE == kDx ? r.col_s : 1.f);
             if (MODE == kLinear) y[j] += r.bias;
         }
     }
