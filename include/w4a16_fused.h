@@ -22,7 +22,8 @@
  * zero before first use (w4a16_workspace_init) and left zero by every
  * completed call, so one workspace can serve all calls of the library that
  * are ordered on one stream, captured graphs among them.  Calls that may
- * overlap need a workspace each.
+ * overlap need a workspace each, and so do, as in w4a16.h, forward calls on
+ * up to 16 tokens with N > 8,388,480, whose counters lie beyond that area.
  */
 #ifndef W4A16_FUSED_H
 #define W4A16_FUSED_H
@@ -43,10 +44,12 @@ typedef enum {
     W4A16_ACT_GELU_TANH = 4
 } w4a16_act;
 
-/* Bytes of device workspace for w4a16_linear_fused and w4a16_gated (N: weight rows), 0 for an invalid shape. */
+/* Bytes of device workspace for w4a16_linear_fused and w4a16_gated on up to M tokens (N: weight rows), 0 for an invalid
+ * shape.  Several layers share a workspace of the largest of their sizes. */
 W4A16_API size_t w4a16_fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 
-/* Bytes of device workspace for w4a16_linear_dx and w4a16_gated_backward (N: weight rows), 0 for an invalid shape. */
+/* Bytes of device workspace for w4a16_linear_dx and w4a16_gated_backward on up to M tokens (N: weight rows), 0 for an
+ * invalid shape. */
 W4A16_API size_t w4a16_dx_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 
 /*

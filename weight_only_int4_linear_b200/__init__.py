@@ -253,12 +253,12 @@ def linear_g(X: torch.Tensor, group: int, qweight: torch.Tensor, scales: torch.T
 
 
 def fused_workspace_bytes(M: int, N: int, K: int, group: int = GROUP) -> int:
-    """w4a16_fused_workspace_bytes: for linear_fused and gated (N: weight rows)."""
+    """w4a16_fused_workspace_bytes: for linear_fused and gated on up to M tokens (N: weight rows)."""
     return int(load().w4a16_fused_workspace_bytes(M, N, K, group))
 
 
 def dx_workspace_bytes(M: int, N: int, K: int, group: int = GROUP) -> int:
-    """w4a16_dx_workspace_bytes: for linear_dx and gated_backward (N: weight rows)."""
+    """w4a16_dx_workspace_bytes: for linear_dx and gated_backward on up to M tokens (N: weight rows)."""
     return int(load().w4a16_dx_workspace_bytes(M, N, K, group))
 
 

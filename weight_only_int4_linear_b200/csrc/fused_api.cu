@@ -74,9 +74,14 @@ extern "C" {
 size_t w4a16_fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
     if (check_fused_shape(M, N, K, group) != W4A16_OK) return 0;
     check_device();  // caches the SM count the plans depend on
-    const size_t a = path_bytes(forward_path(M, K, group, false), M, N, K, group);
-    const size_t b = path_bytes(forward_path(M, K, group, true), M, N, K, group);
-    return a > b ? a : b;
+    // what any call of up to M tokens needs: every path's size grows with its tokens, but not from one path to the next
+    size_t need = 0;
+    for (const int64_t m : {(int64_t)1, M < 16 ? M : 16, M})
+        for (const bool scaled : {false, true}) {
+            const size_t b = path_bytes(forward_path(m, K, group, scaled), m, N, K, group);
+            if (b > need) need = b;
+        }
+    return need;
 }
 
 size_t w4a16_dx_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
