@@ -190,3 +190,17 @@ def test_channel_scales_bring_gradients_back_into_the_range(cuda_lib, M, N, K, u
     want, bound = F.dx64(dY.to(F.F8), W, inv)
     assert 1e-30 < float(want.abs().max()) < 1e38
     F.check(_dx(dY, pw, inv), want, bound)
+
+
+@pytest.mark.parametrize("M,N,K,G", [(1, 258, 512, 64), (6, 1030, 1024, 128), (50, 258, 640, 32), (100, 18002, 256, 128),
+                                     (300, 514, 384, 64)])
+def test_gated_backward_with_channel_scales(cuda_lib, M, N, K, G):
+    pw = F.make_weight(N, K, G, seed=K + M, far=True)
+    W, act = F.weight64(pw), F.ACTS[1 + M % 4]
+    inv = torch.exp2(torch.linspace(-3, 3, K, device="cuda")) * 1.1
+    dH, GU = _rand((M, N // 2), M, 1e-2), _rand((M, N), M + 50, 3.0)
+    d, e = F.grads64(dH, GU, act)
+    dGU, dX = _backward(dH, GU, pw, act, inv_s=inv)
+    F.check(dGU, d, e + F.U16 * (d.abs() + e) + F.TINY, "dGU")
+    want, bound = F.dx64(d, W, inv, r_d=2.0 ** -11, size=F.gated_size(dH, GU))
+    F.check(dX, want, bound + (1 + F.U16) * (e @ W.abs()) * inv.double(), "dX")
