@@ -121,9 +121,14 @@ def _check(fn: str, st: int) -> None:
         raise W4A16Error(fn, st)
 
 
+# A device's current stream as a handle without building a Stream object (3 us), where this PyTorch has that function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream) -> int:
-    if stream is None:  # torch.cuda.current_stream().cuda_stream, without building a Stream object (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -283,7 +288,7 @@ def _call(name: str, index: int, stream, *args) -> None:
         raise ValueError(f"stream must be on cuda:{index}, is on {stream.device}")
     fn = getattr(_lib or load(), name)
     if index == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+        st = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(index):
             st = fn(*args, _stream(stream))
