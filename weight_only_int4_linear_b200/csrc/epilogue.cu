@@ -166,8 +166,7 @@ int launch_cc_epilogue(const float* partial, const FusedEpilogue& e, uint16_t* Y
 }
 
 int launch_deal_epilogue(const float* partial, const FusedEpilogue& e, uint16_t* Y, int64_t N, int M, int G,
-                         int units_base, int units_rem, int max_slots, int row_tiles, cudaStream_t stream) {
-    (void)row_tiles;
+                         int units_base, int units_rem, int max_slots, cudaStream_t stream) {
     const DealSlots s{partial, M, G, units_base, units_rem, max_slots};
     const int outs = (int)(e.gated ? N / 2 : N);
     const int64_t items = ceil_div((int64_t)M * outs, kEpThreads), cap = (int64_t)num_sms_current() * 8;

@@ -197,7 +197,7 @@ __device__ __forceinline__ void act_grads(const float (&x)[T], int act, float (&
     }
 }
 
-// One output of the plain epilogue: n the weight row, off = m N + n.
+// One output of the plain epilogue from its sum v.
 __device__ __forceinline__ float linear_epilogue(float v, const FusedEpilogue& e, float bias, float residual) {
     return act_f(v + bias, e.act) + residual;
 }
@@ -211,7 +211,7 @@ int launch_cc_epilogue(const float* partial, const FusedEpilogue& e, uint16_t* Y
                        int tiles_a, int cpt_b, cudaStream_t stream);
 // 2-16 tokens: slots [tile][max_slots][M][128], every row tile's sums in slots.
 int launch_deal_epilogue(const float* partial, const FusedEpilogue& e, uint16_t* Y, int64_t N, int M, int G,
-                         int units_base, int units_rem, int max_slots, int row_tiles, cudaStream_t stream);
+                         int units_base, int units_rem, int max_slots, cudaStream_t stream);
 
 // The FP16-operand GEMM (gemm_h.cu), any M, K a multiple of 128, groups of 32, 64 or 128.
 size_t gemm_h_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, bool backward, int num_sms);

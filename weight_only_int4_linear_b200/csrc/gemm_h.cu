@@ -31,8 +31,9 @@
 //
 // Work: full waves of tiles run whole, so that the clusters sweep the same
 // operands together (L2); the last, partial wave's tiles, where it pays, are cut
-// along the contraction into equal ranges over all clusters, whose FP32 partial
-// tiles a dependent kernel adds in a fixed order.
+// along the contraction into equal ranges over the clusters (as many as get at least
+// 256 of contraction each), whose FP32 partial tiles a dependent kernel adds in a fixed
+// order.
 //
 // Gated weights (I gate rows, then I up rows) are read interleaved by a 3-D
 // tensor map, row 2 j + p = row p I + j, so that a pair of neighbouring lanes
@@ -761,7 +762,7 @@ struct HArgs {
     FusedEpilogue ep;
     int64_t I;            // gated: rows per half
     int M, R, C;          // tokens, output rows, contraction
-    int Rp, GQ, group, N; // meta stride, groups per weight row, group size, weight rows
+    int GQ, group;        // groups per weight row, group size
     int NS;               // stages per tile
     int m_tiles, r_tiles;
     int whole_tiles;      // tiles 0 .. whole_tiles - 1 run whole: cluster b takes b, b + units, ...
@@ -1401,7 +1402,7 @@ int launch_pdl(Kern kernel, int64_t grid, int block, cudaStream_t stream, Args..
 
 template <int W, bool GATED, int TH>
 int launch_grad_as(GradArgs g, int64_t M, cudaStream_t stream) {
-    // few tokens of long rows: up to 8 blocks a token, while that gives no more blocks than SMs
+    // few tokens of long rows: up to 8 blocks a token, doubled while there are no more blocks than SMs
     const int64_t steps = ceil_div(GATED ? g.I : g.N, TH * 8);
     g.blocks = 1;
     while (g.blocks < 8 && g.blocks < steps && M * g.blocks <= num_sms_current()) g.blocks *= 2;
@@ -1409,7 +1410,10 @@ int launch_grad_as(GradArgs g, int64_t M, cudaStream_t stream) {
 }
 // Threads per block: 128 for many tokens of short rows (a block's fixed cost is then most of it); else 512, or 256 for
 // plain gradients of many tokens in 16-byte loads (4096 x 10240: 35.2 us against 41.3; 100 x 7680: 6.0 against 4.6; gated
-// 2048 x 57344: 186-202 against 176).
+// 2048 x 57344: 186-202 against 176).  us with 128 / 256 / 512 threads, rows of 2048: plain 160 tokens 3.5 / 2.7 / 2.9, 300
+// 3.7 / 3.0 / 3.2, 600 4.0 / 3.4 / 4.9, 4096 11.4 / 12.2 / 19.6; gated 160 6.0 / 4.5 / 4.8, 300 6.5 / 5.5 / 7.5, 4096 28 /
+// 32 / 49; rows of 4096: plain 600 tokens 6.3 / 5.1 / 5.8, 4096 18.9 / 19.4 / 23.8; gated 600 13.3 / 13.0 / 13.4, 4096 51 /
+// 54 / 63.
 template <int W, bool GATED>
 int launch_grad_wide(const GradArgs& g, int64_t M, cudaStream_t stream) {
     const int64_t sms = num_sms_current(), n = GATED ? g.I : g.N;
@@ -1531,10 +1535,8 @@ int launch_gemm_h(const uint16_t* X, const float* xscale, int64_t M, int64_t K, 
     a.M = (int)M;
     a.R = (int)N;
     a.C = (int)K;
-    a.Rp = (int)l.Rp;
     a.GQ = (int)(K / group);
     a.group = group;
-    a.N = (int)N;
     a.m_tiles = (int)ceil_div(M, NT);
     a.r_tiles = (int)ceil_div(N, kTileRows);
     const uint32_t stage_k = NT == 256 ? Cfg<kLinear, 256>::kStageK : Cfg<kLinear, 64>::kStageK;
@@ -1584,10 +1586,8 @@ int launch_gemm_h_dx(const uint16_t* dY, const uint16_t* dH, const uint16_t* GU,
     a.M = (int)M;
     a.R = (int)K;
     a.C = (int)N;
-    a.Rp = (int)l.Rp;
     a.GQ = (int)(K / group);
     a.group = group;
-    a.N = (int)N;
     a.m_tiles = (int)ceil_div(M, NT);
     a.r_tiles = (int)ceil_div(K, kTileRows);
     CUtensorMap tx, tq, tm;

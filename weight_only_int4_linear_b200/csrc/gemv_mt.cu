@@ -543,8 +543,7 @@ int launch_decode_mt(const uint16_t* X, const float* xscale, int64_t M, int64_t 
                        : launch_mt_kernel<16>(tq, tsc, tze, args, p.grid, stream);
         if (st != W4A16_OK) return st;
         if (ep) {  // M <= 16: one launch takes all tokens
-            st = launch_deal_epilogue(partial, *ep, Y, N, Mc, G, p.units_base, p.units_rem, p.max_slots, p.row_tiles,
-                                      stream);
+            st = launch_deal_epilogue(partial, *ep, Y, N, Mc, G, p.units_base, p.units_rem, p.max_slots, stream);
             if (st != W4A16_OK) return st;
             continue;
         }
