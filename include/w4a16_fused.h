@@ -18,6 +18,20 @@
  * finite BF16 value is accepted.  The same call on the same inputs gives the
  * same bits.
  *
+ * Operands.  Up to 16 tokens on the integer GEMVs (see w4a16_linear_fused)
+ * weights are exact and activations off by at most 2^-18 of their group's
+ * largest.  The GEMM takes both operands in FP16, scaled by a power of two
+ * per weight row and per token:
+ *   - a weight (q - z) s is off by at most 2^-11 of itself, or 2^-40 |q - z|
+ *     of its row's size where that is more.  The size is the largest of its
+ *     groups' |s| max(|z|, |15 - z|), each factor raised to a power of two;
+ *   - a token's value is exact, or off by 2^-39 of the token's largest value
+ *     where that is more; backward, of the token's largest |dY| times the
+ *     size of the weight's row.  dG and dU: see w4a16_gated_backward.
+ * A group or row of zeros (every code its zero point, or a scale of 0) has no
+ * size: backward a row of zeros counts for nothing, and a group of zeros can
+ * raise its row's size to at most 2^4 times its smallest group's.
+ *
  * Workspaces follow w4a16.h's rule: the first 256 KB hold counters that are
  * zero before first use (w4a16_workspace_init) and left zero by every
  * completed call, so one workspace can serve all calls of the library that

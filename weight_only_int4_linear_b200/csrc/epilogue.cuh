@@ -22,7 +22,7 @@ struct FusedEpilogue {
 };
 
 // 1 / (1 + e^-x), for x above kFar: past it e^-x nears 2^126, where __fdividef gives 0, and e^x itself is the value to
-// 2^-125.  __expf's error grows as 2^-22 |x|, far below the 2^-9 of the BF16 store.
+// 2^-125.  __expf's error grows as 2^-22 |x|, far below the 2^-8 of the BF16 store.
 constexpr float kFar = -87.f;
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 

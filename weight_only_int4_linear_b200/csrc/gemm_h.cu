@@ -13,10 +13,10 @@
 //     column n.
 //   * tokens: row m is scaled by 2^-a_m so that its largest value is in
 //     [2^14, 2^15); BF16 values (8 significant bits) are then exact down to 2^-29
-//     of the row's maximum and lose absolute bits of 2^-40 of it below.
-// Sums run in FP32 in tensor memory over the whole contraction, without a fold
+//     of the row's maximum and are off by up to 2^-39 of it below.
+// Groups and rows of zeros do not enter e_n (preparation, below).  Sums run in FP32 in tensor memory over the whole contraction, without a fold
 // per group, and the exponents come back in the epilogue.  Against rounding
-// (q - z) s to BF16 (2^-9) this keeps the outputs' error at that of their own
+// (q - z) s to BF16 (2^-8) this keeps the outputs' error at that of their own
 // rounding.
 //
 // Tile: 256 output rows (weight rows, or K columns backward) x NT tokens by a
@@ -226,13 +226,13 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
     constexpr int kMetaGroups = kMetaWords / ROWS;
     __shared__ uint32_t s_raw[ROWS][kMetaGroups + 1];  // scale bits, zero point << 16 (0x7FFF: beyond 1024)
     __shared__ int s_exp[ROWS];
+    __shared__ uint32_t s_word[BACK ? ROWS : 1];  // backward: the rows' first codes
     constexpr int RW = ROWS / (kPrepThreads / 32), U = 4 / RW;  // rows per warp, groups of each in flight per lane
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int v0 = block * ROWS, r0 = warp * RW;
     int64_t first[RW];  // the row's first group, -1 past the matrix
     int top[RW], low[RW];  // largest and smallest exponent bound of the row's groups
     uint32_t usual[RW], least[RW];  // largest and smallest scale of the groups with a zero point in 0 .. 15
-    uint32_t word[RW];     // backward: the row's first codes
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
         const int v = v0 + r0 + i;
@@ -241,7 +241,10 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
         low[i] = -kNothing;
         usual[i] = 0u;
         least[i] = 0xFFFFFFFFu;
-        word[i] = BACK && v < a.R ? __ldg(a.qweight + first[i] * a.words) : 0u;
+        if (BACK && lane == 0 && v < a.R)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_word[r0 + i])),
+                         "l"(a.qweight + first[i] * a.words)
+                         : "memory");
     }
     // groups g0 .. g1 - 1 of the warp's rows into shared memory, U groups of each in flight per lane
     auto read = [&](int g0, int g1) {
@@ -278,7 +281,20 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
         }
     };
     for (int g0 = 0; g0 < a.GQ; g0 += kMetaGroups) read(g0, min(g0 + kMetaGroups, a.GQ));
+    if (BACK) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
+    auto set_exp = [&](int r, int t) {  // of the block's row r, its bound t
+        const int e = t == kNothing ? 0 : t - kTopExp;
+        const bool none = BACK && t == kNothing;
+        s_exp[r] = e;
+        a.exps[v0 + r] = (int16_t)(none ? kZeroRow : e);
+        if (BACK) a.pows[v0 + r] = (uint8_t)(none ? 0 : e >= -126 && e <= 127 ? e + 127 : 255);
+    };
+    auto look_at = [&](int64_t group0, int t) {
+        return live_bound(reinterpret_cast<const uint4*>(a.qweight + group0 * a.words), a.scales + group0, a.zeros + group0,
+                          a.GQ, a.words / 4, t);
+    };
+    uint32_t look = 0u;  // backward: the rows whose codes are looked at, after the loop (fewer registers held over the call)
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
         if (least[i] <= 0x7FFFu) {
@@ -286,22 +302,31 @@ __device__ __forceinline__ void meta_block(const MetaArgs& a, int block) {
             low[i] = min(low[i], group_bound(least[i], 0));  // kNothing for a scale of 0: the row is looked at
         }
         int t = __reduce_max_sync(0xFFFFFFFFu, top[i]);
-        bool look = t - __reduce_min_sync(0xFFFFFFFFu, low[i]) > kSpread;
-        if (BACK && first[i] >= 0) {
-            const uint32_t z0 = a.GQ <= kMetaGroups ? s_raw[r0 + i][0] >> 16 : (uint32_t)__ldg(a.zeros + first[i]);
-            look = look || word[i] == 0x11111111u * z0;
+        const bool apart = t - __reduce_min_sync(0xFFFFFFFFu, low[i]) > kSpread;
+        if constexpr (BACK) {
+            look |= apart ? 1u << i : 0u;
+            if (lane == 0) s_exp[r0 + i] = t;
+        } else {
+            if (apart) t = look_at(first[i], t);
+            if (lane == 0) set_exp(r0 + i, t);
         }
-        if (look)
-            t = live_bound(reinterpret_cast<const uint4*>(a.qweight + first[i] * a.words), a.scales + first[i],
-                           a.zeros + first[i], a.GQ, a.words / 4, t);
-        const int e = t == kNothing ? 0 : t - kTopExp;
-        if (lane == 0) {
-            const int v = v0 + r0 + i;
-            const bool none = BACK && t == kNothing;
-            s_exp[r0 + i] = e;
-            a.exps[v] = (int16_t)(none ? kZeroRow : e);
-            if (BACK) a.pows[v] = (uint8_t)(none ? 0 : e >= -126 && e <= 127 ? e + 127 : 255);
+    }
+    if constexpr (BACK) {
+        __syncwarp();
+        const int v = v0 + r0 + lane;  // lane r: the warp's row r
+        bool zeros = false;
+        if (lane < RW && v < a.R) {
+            const uint32_t z0 = a.GQ <= kMetaGroups ? s_raw[r0 + lane][0] >> 16 : (uint32_t)__ldg(a.zeros + (int64_t)v * a.GQ);
+            zeros = s_word[r0 + lane] == 0x11111111u * z0;
         }
+        look |= __ballot_sync(0xFFFFFFFFu, zeros);
+        for (; look; look &= look - 1u) {
+            const int r = r0 + __ffs(look) - 1, t = look_at((int64_t)(v0 + r) * a.GQ, s_exp[r]);
+            __syncwarp();
+            if (lane == 0) s_exp[r] = t;
+        }
+        __syncwarp();
+        if (lane < RW) set_exp(r0 + lane, s_exp[r0 + lane]);
     }
     for (int g0 = 0; g0 < a.GQ; g0 += kMetaGroups) {
         const int g1 = min(g0 + kMetaGroups, a.GQ);
