@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 
 
 # A zero group or row is stored with a scale that says nothing about its values (the quantiser's is 1): it must not decide
-# how the others are scaled.
+# how the others are scaled.  (dx64 takes a row's size from its largest value; the groups of zeros here lie more than 2^4
+# above their row's others and are left out of it, as rows of zeros always are.)
 def _sparse_weight(N, K, G, size, seed, symmetric=False):
     """Weights of one size with rows of zeros as the quantiser stores them, rows whose scales are zero, and rows with one
     or several zero groups, the first and the last among them."""
